@@ -348,6 +348,142 @@ int moe_latent_forward_persistent(const moe_dims *dims, int32_t T, const uint16_
 int moe_latent_forward_noalloc(const moe_dims *dims, int32_t T, const uint16_t *x,
                                const moe_weights *weights, uint16_t *out, void *hip_stream);
 
+/*
+ * 8-bit rows and their products: E4M3 codes (OCP FP8 "fn": largest value
+ * 448, no infinities) with one fp32 scale per 128 consecutive values of a
+ * row, and weights with one fp32 scale per 128 x 128 block. They stand
+ * beside the layer's bf16 pooler and unpooler (moe_fp8_linear) and its FP4
+ * experts (moe_fp8_grouped), for weights stored that way.
+ *
+ * Widths (cols, K) are multiples of 16 up to 65536 and need not be multiples
+ * of 128: the last scale covers what is left. N up to 65536. Rows below
+ * 2^28. Codes, x and weights 16-byte aligned, rows of x 16-byte aligned
+ * (pitches in elements, at most 2^22; MOE_EALIGN); scales, offsets, indices
+ * and out need the alignment of their type only. Zero rows are a no-op.
+ *
+ * moe_fp8_quantize: x [rows][cols] (pitch ldx) of x_type to
+ *   codes  [rows][cols]            e4m3(x * (448 / amax)), nearest even
+ *   scales [rows][ceil(cols/128)]  amax / 448
+ * amax: the largest finite |x| of the group, at least 2^-90. NaN and
+ * infinities become NaN codes and do not raise the scale.
+ * moe_fp8_swiglu: the same of h = silu(gate) * up in fp32; a row of gate_up
+ * holds inter gate values, then inter up values (the rows the gate/up
+ * product of w13 gives).
+ */
+#define MOE_TYPE_BF16 0
+#define MOE_TYPE_F32 1
+int moe_fp8_quantize(int32_t rows, int32_t cols, const void *x, int64_t ldx,
+                     int32_t x_type, uint8_t *codes, float *scales,
+                     void *hip_stream);
+int moe_fp8_swiglu(int32_t rows, int32_t inter, const void *gate_up, int64_t ld,
+                   int32_t type, uint8_t *codes, float *scales,
+                   void *hip_stream);
+
+/* moe_fp8_linear: out[t][n] = sum over blocks b of 128 of
+ *     x_scales[t][b] * w_scales[n/128][b] * sum_{k in b} x[t][k] * w[n][k]
+ *   x [T][K] codes (pitch ldx), x_scales [T][ceil(K/128)],
+ *   w [N][K] codes, w_scales [ceil(N/128)][ceil(K/128)],
+ *   out [T][N] (pitch ldo) of out_type, rounded once from an fp32 sum. */
+int moe_fp8_linear(int32_t T, int32_t N, int32_t K, const uint8_t *x,
+                   int64_t ldx, const float *x_scales, const uint8_t *w,
+                   const float *w_scales, void *out, int64_t ldo,
+                   int32_t out_type, void *hip_stream);
+
+/* moe_fp8_grouped: the same product for every expert over its own rows:
+ * output rows offsets[e] .. offsets[e+1]-1 against expert e's weights.
+ *   offsets   [n_experts+1] int32, device (moe_route's expert_offsets);
+ *             rows outside [offsets[0], offsets[n_experts]) are left as they
+ *             were. Offsets that decrease or leave [0, rows] give unspecified
+ *             rows but no access outside the buffers.
+ *   row_index [rows] int32, device, or NULL: output row i reads row
+ *             row_index[i] / index_div of x (moe_route's sorted_routes with
+ *             index_div = top_k: each route its token's row; an index outside
+ *             x is clamped into it). NULL: row i, index_div 1, x_rows >= rows.
+ *   x [x_rows][K], x_scales [x_rows][ceil(K/128)], w [E][N][K],
+ *   w_scales [E][ceil(N/128)][ceil(K/128)], out [rows][N].
+ * n_experts <= 256; with row_index x_rows * ldx < 2^31. */
+int moe_fp8_grouped(int32_t rows, int32_t n_experts, int32_t N, int32_t K,
+                    const int32_t *offsets, const int32_t *row_index,
+                    int32_t index_div, int32_t x_rows, const uint8_t *x,
+                    int64_t ldx, const float *x_scales, const uint8_t *w,
+                    const float *w_scales, void *out, int64_t ldo,
+                    int32_t out_type, void *hip_stream);
+
+/*
+ * moe_balance_loss -- how evenly the router spreads its tokens, from what
+ * moe_route gives, and moe_balance_loss_backward -- the gradient of the
+ * router logits, for a trainer.
+ *   p = softmax(logits[t]), lse[t] = log(sum_e exp(logits[t][e])),
+ *   c_e = routes to expert e, N = tokens that count,
+ *   f_e = E * c_e / (K * N), P_e = sum_t p[t][e] / N
+ *   losses[0] = sum_e f_e * P_e   (1 when every expert gets the same)
+ *   losses[1] = sum_t lse[t]^2 / N
+ *   logits     [T][E] fp32, 16-byte aligned
+ *   topk_ids   [T][K] int32; ids outside [0, E) are not counted
+ *   token_mask [T] uint8 or NULL: tokens with 0 do not count
+ *   counts     [E+1] int32 out: c_e, then N
+ *   losses     [2] fp32 out
+ * Tokens whose logits are all -inf do not count either. With none that
+ * counts (also T == 0) counts and losses are written as zeros. The same from
+ * run to run, bit for bit.
+ * Backward, f held constant (counts may be sums over several calls or
+ * processes, and are then the whole batch's):
+ *   grad_logits[t][e] = grad_losses[0]/N * p (f_e - sum_j f_j p_j)
+ *       + grad_losses[1]/N * 2 lse p
+ *       + sum over the token's routes k to e of
+ *           topk_w[t][k] * (grad_topk_w[t][k] - sum_j topk_w[t][j] grad_topk_w[t][j])
+ * The last line (the softmax over the selected logits that makes moe_route's
+ * weights) only with topk_w and grad_topk_w, both or neither; without them
+ * topk_ids may be NULL. Tokens that do not count get zeros.
+ *   grad_losses [2] fp32, device.  grad_logits [T][E] fp32 out, 16-byte aligned.
+ * n_experts <= 256, top_k <= min(8, n_experts), T < 2^28. workspace:
+ * moe_balance_workspace_bytes (0 for few tokens: workspace may be NULL).
+ */
+size_t moe_balance_workspace_bytes(int32_t T, int32_t n_experts);
+int moe_balance_loss(int32_t T, int32_t n_experts, int32_t top_k,
+                     const float *logits, const int32_t *topk_ids,
+                     const uint8_t *token_mask, int32_t *counts, float *losses,
+                     void *workspace, size_t workspace_bytes, void *hip_stream);
+int moe_balance_loss_backward(int32_t T, int32_t n_experts, int32_t top_k,
+                              const float *logits, const int32_t *topk_ids,
+                              const uint8_t *token_mask, const int32_t *counts,
+                              const float *grad_losses, const float *topk_w,
+                              const float *grad_topk_w, float *grad_logits,
+                              void *hip_stream);
+
+/* Their argument checks alone (callable without a GPU). */
+int moe_fp8_quantize_validate(int32_t rows, int32_t cols, const void *x,
+                              int64_t ldx, int32_t x_type, const uint8_t *codes,
+                              const float *scales);
+int moe_fp8_swiglu_validate(int32_t rows, int32_t inter, const void *gate_up,
+                            int64_t ld, int32_t type, const uint8_t *codes,
+                            const float *scales);
+int moe_fp8_linear_validate(int32_t T, int32_t N, int32_t K, const uint8_t *x,
+                            int64_t ldx, const float *x_scales, const uint8_t *w,
+                            const float *w_scales, const void *out, int64_t ldo,
+                            int32_t out_type);
+int moe_fp8_grouped_validate(int32_t rows, int32_t n_experts, int32_t N,
+                             int32_t K, const int32_t *offsets,
+                             const int32_t *row_index, int32_t index_div,
+                             int32_t x_rows, const uint8_t *x, int64_t ldx,
+                             const float *x_scales, const uint8_t *w,
+                             const float *w_scales, const void *out, int64_t ldo,
+                             int32_t out_type);
+int moe_balance_loss_validate(int32_t T, int32_t n_experts, int32_t top_k,
+                              const float *logits, const int32_t *topk_ids,
+                              const uint8_t *token_mask, const int32_t *counts,
+                              const float *losses, const void *workspace,
+                              size_t workspace_bytes);
+int moe_balance_loss_backward_validate(int32_t T, int32_t n_experts,
+                                       int32_t top_k, const float *logits,
+                                       const int32_t *topk_ids,
+                                       const uint8_t *token_mask,
+                                       const int32_t *counts,
+                                       const float *grad_losses,
+                                       const float *topk_w,
+                                       const float *grad_topk_w,
+                                       const float *grad_logits);
+
 /* Host-side evaluation of the tile orders of the prefill kernels (tests
  * check them over many shapes; no device work). For launch `kind`:
  *  MOE_TILES_DENSE  (0): the dense projection of an a x b output (pooler,

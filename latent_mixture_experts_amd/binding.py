@@ -103,6 +103,20 @@ def lib():
         L.moe_workspace_view.restype = ctypes.c_int
         L.moe_workspace_view.argtypes = [ctypes.POINTER(MoeDims), _i32, _i32,
                                          ctypes.POINTER(_sz), ctypes.POINTER(_sz)]
+        i64 = ctypes.c_int64
+        for name, args in {
+            "moe_fp8_quantize": [_i32, _i32, _vp, i64, _i32, _vp, _vp],
+            "moe_fp8_swiglu": [_i32, _i32, _vp, i64, _i32, _vp, _vp],
+            "moe_fp8_linear": [_i32, _i32, _i32, _vp, i64, _vp, _vp, _vp, _vp, i64, _i32],
+            "moe_fp8_grouped": [_i32, _i32, _i32, _i32, _vp, _vp, _i32, _i32, _vp, i64, _vp, _vp,
+                                _vp, _vp, i64, _i32],
+            "moe_balance_loss": [_i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz],
+            "moe_balance_loss_backward": [_i32, _i32, _i32] + [_vp] * 8,
+        }.items():
+            for fn, more in ((getattr(L, name), [_vp]), (getattr(L, name + "_validate"), [])):
+                fn.restype, fn.argtypes = ctypes.c_int, args + more
+        L.moe_balance_workspace_bytes.restype = _sz
+        L.moe_balance_workspace_bytes.argtypes = [_i32, _i32]
         L.moe_status_string.restype = ctypes.c_char_p
         L.moe_status_string.argtypes = [ctypes.c_int]
         L.moe_last_hip_error.restype = ctypes.c_int
@@ -261,6 +275,195 @@ def workspace_view(d: MoeDims, T: int, ws: torch.Tensor, which: str, dtype, shap
     """An intermediate of the last moe_latent_forward, viewed in the workspace."""
     off, nb = workspace_view_range(d, T, which)
     return ws[off:off + nb].view(dtype).view(shape)
+
+
+# ---- 8-bit rows, their products, the balance loss --------------------------
+# These take their sizes from the tensors, so they check them: a wrong shape,
+# type, layout or device raises ValueError before anything is enqueued. They
+# run on the tensors' device, on its current stream unless one is given.
+TYPE_BF16, TYPE_F32 = 0, 1  # MOE_TYPE_*
+_FLOATS = {torch.bfloat16: TYPE_BF16, torch.int16: TYPE_BF16, torch.float32: TYPE_F32}  # int16: bf16 bits
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _check(name: str, t: torch.Tensor, dev: torch.device, types, shape, pitched: bool = False) -> None:
+    """t is on dev, of one of the types, of that shape, and dense (pitched: its rows are, at any pitch)."""
+    if (t.device != dev or t.dtype not in types or t.shape != shape or
+            not (t.is_contiguous() or (pitched and (t.shape[1] == 1 or t.stride(1) == 1)
+                                       and t.stride(0) >= t.shape[1]))):
+        raise ValueError(f"{name}: needs {'rows' if pitched else 'a dense tensor'} {list(shape)} of "
+                         f"{' or '.join(str(x) for x in types)} on {dev}, got {list(t.shape)} {t.dtype} "
+                         f"on {t.device}, strides {t.stride()}")
+
+
+def _pitch(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _run(what: str, dev: torch.device, stream, *args) -> None:
+    fn = getattr(lib(), what)
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(stream))
+    if rc != MOE_OK:
+        raise MoeError(rc, what)
+
+
+def _device(t: torch.Tensor) -> torch.device:
+    _need(t.is_cuda, "the tensors must be on a GPU")
+    return t.device
+
+
+def _quantize(what: str, x: torch.Tensor, cols: int, codes, scales, stream):
+    dev = _device(x)
+    rows = x.shape[0]
+    _check("x", x, dev, tuple(_FLOATS), (rows, x.shape[1]), pitched=True)
+    if codes is None:
+        codes = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
+    else:
+        _check("codes", codes, dev, _CODES, (rows, cols))
+    if scales is None:
+        scales = torch.empty((rows, _blocks(cols)), dtype=torch.float32, device=dev)
+    else:
+        _check("scales", scales, dev, (torch.float32,), (rows, _blocks(cols)))
+    _run(what, dev, stream, rows, cols, x.data_ptr(), _pitch(x), _FLOATS[x.dtype], codes.data_ptr(),
+         scales.data_ptr())
+    return codes, scales
+
+
+def fp8_quantize(x: torch.Tensor, codes=None, scales=None, stream=None):
+    """moe_fp8_quantize of x [rows][cols] (bf16 or fp32, rows at any pitch):
+    (codes [rows][cols] e4m3, scales [rows][ceil(cols/128)] fp32)."""
+    _need(x.dim() == 2, "x: needs two dimensions")
+    return _quantize("moe_fp8_quantize", x, x.shape[1], codes, scales, stream)
+
+
+def fp8_swiglu(gate_up: torch.Tensor, codes=None, scales=None, stream=None):
+    """moe_fp8_swiglu of gate_up [rows][2 * inter] (gate values, then up
+    values): silu(gate) * up as fp8_quantize gives it."""
+    _need(gate_up.dim() == 2 and gate_up.shape[1] % 2 == 0, "gate_up: needs two dimensions, the second even")
+    return _quantize("moe_fp8_swiglu", gate_up, gate_up.shape[1] // 2, codes, scales, stream)
+
+
+def _out(out, rows: int, n: int, dtype, dev: torch.device) -> torch.Tensor:
+    if out is None:
+        _need(dtype in _FLOATS, f"out_dtype: bfloat16 or float32, got {dtype}")
+        return torch.empty((rows, n), dtype=dtype, device=dev)
+    _check("out", out, dev, tuple(_FLOATS), (rows, n), pitched=True)
+    return out
+
+
+def fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+               out_dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+    """moe_fp8_linear: x [T][K] e4m3 with x_scales [T][ceil(K/128)], times w
+    [N][K] e4m3 with w_scales [ceil(N/128)][ceil(K/128)] -> [T][N] of
+    out_dtype, or into out. Rows of x and out at any pitch."""
+    _need(x.dim() == 2 and w.dim() == 2, "x, w: need two dimensions")
+    dev = _device(x)
+    (T, K), N = x.shape, w.shape[0]
+    _check("x", x, dev, _CODES, (T, K), pitched=True)
+    _check("x_scales", x_scales, dev, (torch.float32,), (T, _blocks(K)))
+    _check("w", w, dev, _CODES, (N, K))
+    _check("w_scales", w_scales, dev, (torch.float32,), (_blocks(N), _blocks(K)))
+    out = _out(out, T, N, out_dtype, dev)
+    _run("moe_fp8_linear", dev, stream, T, N, K, x.data_ptr(), _pitch(x), x_scales.data_ptr(),
+         w.data_ptr(), w_scales.data_ptr(), out.data_ptr(), _pitch(out), _FLOATS[out.dtype])
+    return out
+
+
+def fp8_grouped(x: torch.Tensor, x_scales: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
+                w_scales: torch.Tensor, out_dtype=torch.bfloat16, row_index=None, index_div: int = 1,
+                out=None, stream=None) -> torch.Tensor:
+    """moe_fp8_grouped: rows offsets[e] .. offsets[e+1]-1 times expert e's
+    weights, w [E][N][K] with w_scales [E][ceil(N/128)][ceil(K/128)], offsets
+    [E+1] int32. The rows are those of x, or with row_index [rows] int32 row
+    row_index[i] // index_div of x for output row i."""
+    _need(x.dim() == 2 and w.dim() == 3, "x: needs two dimensions, w three")
+    dev = _device(x)
+    (x_rows, K), (E, N, _) = x.shape, w.shape
+    rows = x_rows
+    _check("x", x, dev, _CODES, (x_rows, K), pitched=True)
+    _check("x_scales", x_scales, dev, (torch.float32,), (x_rows, _blocks(K)))
+    _check("offsets", offsets, dev, (torch.int32,), (E + 1,))
+    _check("w", w, dev, _CODES, (E, N, K))
+    _check("w_scales", w_scales, dev, (torch.float32,), (E, _blocks(N), _blocks(K)))
+    if row_index is not None:
+        rows = row_index.numel()
+        _check("row_index", row_index, dev, (torch.int32,), (rows,))
+    out = _out(out, rows, N, out_dtype, dev)
+    _run("moe_fp8_grouped", dev, stream, rows, E, N, K, offsets.data_ptr(), _ptr(row_index), index_div,
+         x_rows, x.data_ptr(), _pitch(x), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
+         out.data_ptr(), _pitch(out), _FLOATS[out.dtype])
+    return out
+
+
+def balance_workspace_bytes(T: int, n_experts: int) -> int:
+    return int(lib().moe_balance_workspace_bytes(T, n_experts))
+
+
+def balance_loss(logits: torch.Tensor, ids: torch.Tensor, mask=None, ws=None, stream=None):
+    """moe_balance_loss of logits [T][E] fp32 and ids [T][K] int32, mask [T]
+    uint8 or bool (tokens that count; None: all): (losses [2] fp32: balance,
+    z; counts [E+1] int32: routes per expert, tokens that counted). ws: a
+    uint8 workspace of balance_workspace_bytes, allocated here if None."""
+    _need(logits.dim() == 2 and ids.dim() == 2, "logits, ids: need two dimensions")
+    dev = _device(logits)
+    (T, E), K = logits.shape, ids.shape[1]
+    _check("logits", logits, dev, (torch.float32,), (T, E))
+    _check("ids", ids, dev, (torch.int32,), (T, K))
+    if mask is not None:
+        _check("mask", mask, dev, (torch.uint8, torch.bool), (T,))
+    if ws is None:
+        n = balance_workspace_bytes(T, E)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    else:
+        _check("ws", ws, dev, (torch.uint8,), (ws.numel(),))
+    losses = torch.empty(2, dtype=torch.float32, device=dev)
+    counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    _run("moe_balance_loss", dev, stream, T, E, K, logits.data_ptr(), ids.data_ptr(), _ptr(mask),
+         counts.data_ptr(), losses.data_ptr(), _ptr(ws), ws.numel() if ws is not None else 0)
+    return losses, counts
+
+
+def balance_loss_backward(logits: torch.Tensor, ids: torch.Tensor, counts: torch.Tensor,
+                          grad_losses: torch.Tensor, mask=None, w=None, grad_w=None, out=None,
+                          stream=None) -> torch.Tensor:
+    """moe_balance_loss_backward: the gradient [T][E] fp32 of the logits
+    through both losses (grad_losses [2] fp32 on the device, counts as
+    balance_loss gave them or summed over processes) and, with w and grad_w
+    [T][K] fp32, through the router weights."""
+    _need(logits.dim() == 2 and ids.dim() == 2, "logits, ids: need two dimensions")
+    dev = _device(logits)
+    (T, E), K = logits.shape, ids.shape[1]
+    f32 = (torch.float32,)
+    _check("logits", logits, dev, f32, (T, E))
+    _check("ids", ids, dev, (torch.int32,), (T, K))
+    _check("counts", counts, dev, (torch.int32,), (E + 1,))
+    _check("grad_losses", grad_losses, dev, f32, (2,))
+    if mask is not None:
+        _check("mask", mask, dev, (torch.uint8, torch.bool), (T,))
+    _need((w is None) == (grad_w is None), "w, grad_w: both or neither")
+    if w is not None:
+        _check("w", w, dev, f32, (T, K))
+        _check("grad_w", grad_w, dev, f32, (T, K))
+    if out is None:
+        out = torch.empty((T, E), dtype=torch.float32, device=dev)
+    else:
+        _check("out", out, dev, f32, (T, E))
+    _run("moe_balance_loss_backward", dev, stream, T, E, K, logits.data_ptr(), ids.data_ptr(), _ptr(mask),
+         counts.data_ptr(), grad_losses.data_ptr(), _ptr(w), _ptr(grad_w), out.data_ptr())
+    return out
 
 
 # ---- HIP events (timing of the stages on the stream they run on) ----------

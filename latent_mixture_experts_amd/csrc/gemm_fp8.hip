@@ -1,0 +1,478 @@
+// gemm_fp8.hip -- products of E4M3 rows with E4M3 weights, one fp32 scale per
+// 128 values of a row and one per 128 x 128 block of the weights, dense and
+// per expert.
+//
+//   out[r][n] = sum_b xs[r][b] * ws[n/128][b] * sum_{k in block b} x[r][k] w[n][k]
+//
+// A block's sum leaves the matrix unit before it meets its scales (a scale that
+// is no power of two cannot enter it) and is added in fp32 on the vector unit.
+// The weights are the A operand and the rows the B operand, so a lane holds
+// four neighbouring outputs of ONE row: its scale product is one value per row
+// fragment and block, not one per output.
+//
+// Two ways to sum a block. The E4M3 MFMA 16x16x128 takes it in one
+// instruction at twice the bf16 rate, but adds its products on a grid set by
+// the largest of them (measured: a block's sum off by up to 2^-11 of its largest
+// product, 1.5e-5 of the sums' norm for normal operands): enough for outputs
+// rounded to bf16 (2^-9 each), not for fp32 ones. There, and wherever the
+// weights' way from HBM bounds the kernel anyway, the codes become bf16 (exact)
+// and four bf16 MFMAs 16x16x32 sum the block to fp32 (measured: 1e-8 of the norm).
+#include "device_common.h"
+#include "fp8.h"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// Eight E4M3 codes as bf16, exactly.
+__device__ __forceinline__ bf16x8 e4m3x8_to_bf16(int lo, int hi) {
+  const uint32_t l = static_cast<uint32_t>(lo), h = static_cast<uint32_t>(hi);
+  const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(l, 1.0f, false);
+  const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(l, 1.0f, true);
+  const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(h, 1.0f, false);
+  const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(h, 1.0f, true);
+  return bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
+// D(16x16, fp32) = A(16x128, E4M3) * B(128x16, E4M3). Lane l supplies row
+// l%16 of A and column l%16 of B; the 32 bytes of lane group l/16 may be any
+// 32 of the block's 128 as long as both operands take the same ones, since
+// the block is summed whole. It receives D rows 4*(l/16) .. +3 of column l%16.
+// EXACT: through bf16.
+template <bool EXACT>
+__device__ __forceinline__ f32x4 mfma_block(i32x8 a, i32x8 b) {
+  f32x4 d{0.f, 0.f, 0.f, 0.f};
+  if constexpr (!EXACT) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, d, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    d = mfma16x16x32(e4m3x8_to_bf16(a[2 * s], a[2 * s + 1]), e4m3x8_to_bf16(b[2 * s], b[2 * s + 1]), d);
+  return d;
+}
+
+__device__ __forceinline__ i32x8 pair16(uint4 lo, uint4 hi) {
+  return i32x8{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z), static_cast<int>(lo.w),
+               static_cast<int>(hi.x), static_cast<int>(hi.y), static_cast<int>(hi.z), static_cast<int>(hi.w)};
+}
+
+// The rows a workgroup takes: tile `tile` of the list that gives every
+// expert ceil(rows / tile_rows) tiles, experts ascending. Every wavefront
+// finds it by itself: four experts per lane, a scan of the tile counts over
+// the lanes, a ballot. Offsets are clamped into [0, rows], so a bad list
+// cannot lead outside the buffers. expert < 0: no such tile.
+struct Group {
+  int expert, begin, end;
+};
+__device__ __forceinline__ Group find_group(const Fp8Gemm& p, int tile, int tile_rows) {
+  if (!p.offsets) {
+    const int b = tile * tile_rows;
+    return b < p.rows ? Group{0, b, min(p.rows - b, tile_rows) + b} : Group{-1, 0, 0};
+  }
+  const int lane = threadIdx.x & 63;
+  int off[5], cnt[4], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 5; ++i) off[i] = min(max(p.offsets[min(4 * lane + i, p.experts)], 0), p.rows);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = off[i + 1] - off[i];
+    cnt[i] = n > 0 ? (n - 1) / tile_rows + 1 : 0;  // (lanes past the last expert: no rows)
+    sum += cnt[i];
+  }
+  int upto = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int v = __shfl_up(upto, d, 64);
+    if (lane >= d) upto += v;
+  }
+  int left = tile - (upto - sum);
+  const uint64_t mine = __ballot(left >= 0 && left < sum);
+  if (mine == 0) return Group{-1, 0, 0};
+  int e = 4 * lane, b = off[0], n = off[1];
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    if (e == 4 * lane + i && left >= cnt[i]) {
+      left -= cnt[i];
+      e = 4 * lane + i + 1;
+      b = off[i + 1];
+      n = off[i + 2];
+    }
+  b += left * tile_rows;
+  const int src = __builtin_ctzll(mine);
+  Group g;
+  g.expert = __builtin_amdgcn_readlane(e, src);
+  g.begin = __builtin_amdgcn_readlane(b, src);
+  g.end = min(__builtin_amdgcn_readlane(n, src), g.begin + min(tile_rows, p.rows));
+  return g;
+}
+
+// The row of x that output row r reads (an index outside x is clamped into it).
+__device__ __forceinline__ int source_row(const Fp8Gemm& p, int r) {
+  if (!p.index) return r;
+  const int v = p.index[r] / p.index_div;
+  return min(max(v, 0), p.x_rows - 1);
+}
+
+// Four neighbouring outputs n .. n+3 of one row.
+template <bool F32>
+__device__ __forceinline__ void store4(const Fp8Gemm& p, int row, int n, f32x4 v) {
+  const size_t at = static_cast<size_t>(row) * p.ldo + n;
+  if constexpr (F32) {
+    float* o = static_cast<float*>(p.out) + at;
+    if (p.out_vec && n + 4 <= p.N) {
+      *reinterpret_cast<f32x4*>(o) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < p.N) o[i] = v[i];
+    }
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(p.out) + at;
+    if (p.out_vec && n + 4 <= p.N) {
+      *reinterpret_cast<uint2*>(o) =
+          uint2{f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16),
+                f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16)};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < p.N) o[i] = f32_to_bf16(v[i]);
+    }
+  }
+}
+
+// ---- few rows: the weights stream once from HBM ----------------------------
+// Workgroup: 16 weight rows x up to 16 * F rows, the blocks of K split over
+// its eight wavefronts (consecutive runs) and joined through LDS in wavefront
+// order. A group of more rows takes them in passes. Grid: (weight row tiles,
+// groups).
+constexpr int kFW = 8;  // wavefronts
+constexpr int kFU = 4;  // blocks loaded together, one such set ahead of the products
+
+template <int F, bool F32>
+__global__ __launch_bounds__(64 * kFW) void fp8_stream_kernel(Fp8Gemm p) {
+  __shared__ f32x4 part[kFW][F][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nl = lane & 15, g = lane >> 4;
+  const Group grp = p.offsets ? find_group(p, static_cast<int>(blockIdx.y), 1 << 30) : Group{0, 0, p.rows};
+  if (grp.expert < 0) return;
+  const int n0 = static_cast<int>(blockIdx.x) * 16;
+  const int nkb = (p.K + kFp8Block - 1) / kFp8Block;
+  const int per = (nkb + kFW - 1) / kFW;
+  const int kb0 = wave * per, kb1 = min(kb0 + per, nkb);
+  const size_t K = static_cast<size_t>(p.K);
+  const rsrc_t w_r = make_rsrc(p.w + (static_cast<size_t>(grp.expert) * p.N + n0) * K,
+                               static_cast<uint32_t>(min(16, p.N - n0) * K));
+  const float* ws = p.ws + (static_cast<size_t>(grp.expert) * ((p.N + kFp8Block - 1) / kFp8Block) + n0 / kFp8Block) * nkb;
+  const uint32_t w_off = static_cast<uint32_t>(nl) * p.K + g * 16;
+
+  for (int r0 = grp.begin; r0 < grp.end; r0 += 16 * F) {
+    const int base = p.index ? 0 : r0;  // the descriptors start at this row of x
+    const int rows_here = p.index ? p.x_rows : grp.end - r0;
+    const rsrc_t x_r = make_rsrc(p.x + static_cast<size_t>(base) * p.ldx,
+                                 static_cast<uint32_t>(static_cast<size_t>(min(rows_here, p.index ? rows_here : 16 * F) - 1) * p.ldx + K));
+    uint32_t x_off[F];
+    const float* xs[F];
+    bool live[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      const int r = r0 + f * 16 + nl;
+      live[f] = r < grp.end;
+      const int src = live[f] ? source_row(p, r) : base;
+      x_off[f] = live[f] ? static_cast<uint32_t>((src - base) * p.ldx) + g * 16 : kOutOfRange;
+      xs[f] = p.xs + static_cast<size_t>(src) * nkb;
+    }
+    f32x4 acc[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    uint4 wv[2][kFU][2];
+    // (blocks past this wavefront's run and pieces past the last value read
+    // nothing and give zeros)
+    auto at = [&](uint32_t off, int kb, int half) -> uint32_t {
+      const int k = kb * kFp8Block + half * 64 + g * 16;
+      return kb < kb1 && k < p.K ? off + kb * kFp8Block + half * 64 : kOutOfRange;
+    };
+    auto load_w = [&](int kb, int set) __attribute__((always_inline)) {
+#pragma unroll
+      for (int u = 0; u < kFU; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) wv[set][u][h] = buf_load16<kAuxStream>(w_r, at(w_off, kb + u, h));
+    };
+    auto step = [&](int kb, int set) __attribute__((always_inline)) {
+      if (kb + kFU < kb1) load_w(kb + kFU, set ^ 1);
+      uint4 xv[F][kFU][2];
+      float sc[F][kFU];
+#pragma unroll
+      for (int u = 0; u < kFU; ++u) {
+        const int kc = min(kb + u, nkb - 1);
+        const float wsc = ws[kc];
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            xv[f][u][h] = buf_load16<kAuxDefault>(x_r, live[f] ? at(x_off[f], kb + u, h) : kOutOfRange);
+          sc[f][u] = xs[f][kc] * wsc;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kFU; ++u) {
+        if (kb + u >= kb1) break;  // (uniform)
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          const f32x4 d = mfma_block<true>(pair16(wv[set][u][0], wv[set][u][1]), pair16(xv[f][u][0], xv[f][u][1]));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[f][i] = fmaf(d[i], sc[f][u], acc[f][i]);
+        }
+      }
+    };
+    if (kb0 < kb1) load_w(kb0, 0);
+    for (int kb = kb0; kb < kb1; kb += 2 * kFU) {
+      step(kb, 0);
+      if (kb + kFU < kb1) step(kb + kFU, 1);
+    }
+#pragma unroll
+    for (int f = 0; f < F; ++f) part[wave][f][lane] = acc[f];
+    __syncthreads();
+    if (wave < F) {
+      f32x4 s = part[0][wave][lane];
+#pragma unroll
+      for (int v = 1; v < kFW; ++v) s += part[v][wave][lane];
+      const int r = r0 + wave * 16 + nl;
+      if (r < grp.end) store4<F32>(p, r, n0 + 4 * g, s);
+    }
+    __syncthreads();  // (the next pass writes part again)
+  }
+}
+
+// ---- many rows: LDS-staged tiles -------------------------------------------
+// Workgroup tile: WT x WW wavefronts, each FT x FW fragments of 16 rows x 16
+// weight rows. One block of K per stage: both operands' 128-byte rows are
+// copied straight from global memory into LDS (two stages, the copies of the
+// next under the products of this one), 16-byte piece c of row r at position
+// r*8 + (c ^ ((r/2) % 8)), so that the 16 rows one read touches start in
+// distinct banks. The scales follow in LDS in sets of four stages, loaded to
+// registers one set ahead.
+constexpr int kFSet = 4;
+
+__device__ __forceinline__ int fpos(int r, int c) { return (r * 8 + (c ^ ((r >> 1) & 7))) * 16; }
+
+template <int WT, int WW, int FT, int FW, bool F32>
+__global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n_row_tiles, int n_col_tiles) {
+  constexpr int NW = WT * WW, BM = WT * FT * 16, BN = WW * FW * 16;
+  constexpr int kXOps = BM / 8 / NW, kWOps = BN / 8 / NW;  // 1-KiB copies per wavefront and stage
+  constexpr int kThreads = 64 * NW;
+  constexpr int kNB = BN / kFp8Block;                       // weight blocks across the tile
+  constexpr int kSets = kFSet * (BM + kNB);                 // scales of one set
+  constexpr int kPer = (kSets + kThreads - 1) / kThreads;
+  static_assert(BN % kFp8Block == 0 && kXOps * 8 * NW == BM && kWOps * 8 * NW == BN, "whole copies");
+  __shared__ __attribute__((aligned(1024))) uint8_t Xs[2][BM * kFp8Block];
+  __shared__ __attribute__((aligned(1024))) uint8_t Ws[2][BN * kFp8Block];
+  __shared__ float Sc[2][kSets];  // [set parity][stage in set][row, then weight block]
+  __shared__ int src[BM];         // source row of each tile row
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nl = lane & 15, g = lane >> 4;
+  const int wt = wave % WT, ww = wave / WT;
+
+  int mt, nt;
+  if (p.offsets) {  // an expert's row tiles share its weights in one XCD's L2
+    const int logical = xcd_tile(2 * n_col_tiles);
+    mt = logical / n_col_tiles;
+    nt = logical % n_col_tiles;
+  } else {
+    const TileRC t = dense_tile_of(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), n_row_tiles,
+                                   n_col_tiles, 4);
+    mt = t.mt;
+    nt = t.nt;
+    if (mt < 0) return;
+  }
+  const Group grp = find_group(p, mt, BM);
+  if (grp.expert < 0) return;
+  const int nrows = grp.end - grp.begin, n0 = nt * BN, ncols = min(BN, p.N - n0);
+  const int nkb = (p.K + kFp8Block - 1) / kFp8Block;
+  const size_t K = static_cast<size_t>(p.K);
+  const rsrc_t w_r = make_rsrc(p.w + (static_cast<size_t>(grp.expert) * p.N + n0) * K, static_cast<uint32_t>(ncols * K));
+  const float* ws = p.ws + (static_cast<size_t>(grp.expert) * ((p.N + kFp8Block - 1) / kFp8Block) + n0 / kFp8Block) * nkb;
+  const int base = p.index ? 0 : grp.begin;
+  const rsrc_t x_r = make_rsrc(p.x + static_cast<size_t>(base) * p.ldx,
+                               static_cast<uint32_t>(static_cast<size_t>((p.index ? p.x_rows : nrows) - 1) * p.ldx + K));
+  for (int r = tid; r < BM; r += kThreads) src[r] = r < nrows ? source_row(p, grp.begin + r) : -1;
+  __syncthreads();
+
+  // source offsets of this wavefront's copies, and this lane's value offset in a block
+  uint32_t xoff[kXOps], woff[kWOps];
+  int xk[kXOps], wk[kWOps];
+#pragma unroll
+  for (int i = 0; i < kXOps; ++i) {
+    const int r = (kXOps * wave + i) * 8 + (lane >> 3);
+    xk[i] = ((lane & 7) ^ ((r >> 1) & 7)) * 16;
+    xoff[i] = src[r] < 0 ? kOutOfRange : static_cast<uint32_t>((src[r] - base) * p.ldx) + xk[i];
+  }
+#pragma unroll
+  for (int i = 0; i < kWOps; ++i) {
+    const int r = (kWOps * wave + i) * 8 + (lane >> 3);
+    wk[i] = ((lane & 7) ^ ((r >> 1) & 7)) * 16;
+    woff[i] = static_cast<uint32_t>(r) * p.K + wk[i];
+  }
+  const uint32_t lds_x = static_cast<uint32_t>(reinterpret_cast<size_t>(
+      (__attribute__((address_space(3))) uint8_t*)(&Xs[0][0])));
+  const uint32_t lds_w = static_cast<uint32_t>(reinterpret_cast<size_t>(
+      (__attribute__((address_space(3))) uint8_t*)(&Ws[0][0])));
+  auto issue = [&](int st, int slot) __attribute__((always_inline)) {
+    const int k0 = st * kFp8Block;
+    // (pieces past the last value read nothing: zeros in both operands)
+#pragma unroll
+    for (int i = 0; i < kXOps; ++i)
+      lds_copy16(x_r, xk[i] + k0 < p.K ? xoff[i] + k0 : kOutOfRange,
+                 __builtin_amdgcn_readfirstlane(lds_x + slot * (BM * kFp8Block) + (kXOps * wave + i) * 1024));
+#pragma unroll
+    for (int i = 0; i < kWOps; ++i)
+      lds_copy16(w_r, wk[i] + k0 < p.K ? woff[i] + k0 : kOutOfRange,
+                 __builtin_amdgcn_readfirstlane(lds_w + slot * (BN * kFp8Block) + (kWOps * wave + i) * 1024));
+  };
+
+  // scales of one set: this thread's kPer of them
+  const float* sp[kPer];
+  int sq[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = tid + j * kThreads, c = i / kFSet;  // four consecutive threads: one row's four stages
+    sq[j] = i % kFSet;
+    if (i >= kSets)
+      sp[j] = nullptr;
+    else if (c < BM)
+      sp[j] = src[c] < 0 ? nullptr : p.xs + static_cast<size_t>(src[c]) * nkb;
+    else
+      sp[j] = (c - BM) * kFp8Block < ncols ? ws + static_cast<size_t>(c - BM) * nkb : nullptr;
+  }
+  float sv[kPer];
+  auto load_set = [&](int set) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int kb = set * kFSet + sq[j];
+      sv[j] = sp[j] && kb < nkb ? sp[j][kb] : 0.0f;
+    }
+  };
+  auto store_set = [&](int set) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = tid + j * kThreads;
+      if (i < kSets) Sc[set & 1][sq[j] * (BM + kNB) + i / kFSet] = sv[j];
+    }
+  };
+
+  f32x4 acc[FT][FW];
+#pragma unroll
+  for (int t = 0; t < FT; ++t)
+#pragma unroll
+    for (int f = 0; f < FW; ++f) acc[t][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  auto compute = [&](int st, int slot, auto live_tag) __attribute__((always_inline)) {
+    constexpr int LIVE = decltype(live_tag)::value;
+    if constexpr (LIVE > 0) {
+      const float* sc = &Sc[(st / kFSet) & 1][(st % kFSet) * (BM + kNB)];
+      const float wsc = sc[BM + ww * (FW * 16) / kFp8Block];
+      i32x8 wv[FW];
+#pragma unroll
+      for (int f = 0; f < FW; ++f) {
+        const int r = (ww * FW + f) * 16 + nl;
+        wv[f] = pair16(*reinterpret_cast<const uint4*>(&Ws[slot][fpos(r, g)]),
+                       *reinterpret_cast<const uint4*>(&Ws[slot][fpos(r, 4 + g)]));
+      }
+#pragma unroll
+      for (int t = 0; t < LIVE; ++t) {
+        const int r = (wt * FT + t) * 16 + nl;
+        const i32x8 xv = pair16(*reinterpret_cast<const uint4*>(&Xs[slot][fpos(r, g)]),
+                                *reinterpret_cast<const uint4*>(&Xs[slot][fpos(r, 4 + g)]));
+        const float s = sc[r] * wsc;
+#pragma unroll
+        for (int f = 0; f < FW; ++f) {
+          const f32x4 d = mfma_block<F32>(wv[f], xv);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][f][i] = fmaf(d[i], s, acc[t][f][i]);
+        }
+      }
+    }
+  };
+
+  auto kloop = [&](auto live_tag) __attribute__((always_inline)) {
+    load_set(0);
+    issue(0, 0);
+    store_set(0);
+    wait_vm_keep<0>();
+    __syncthreads();
+    for (int st = 0; st < nkb; ++st) {
+      const int slot = st & 1;
+      if (st + 1 < nkb) issue(st + 1, slot ^ 1);
+      const bool first = st % kFSet == 0, last = st % kFSet == kFSet - 1;
+      if (first) load_set(st / kFSet + 1);
+      compute(st, slot, live_tag);
+      if (last) store_set(st / kFSet + 1);
+      wait_vm_keep<0>();  // stage st + 1 has landed
+      __syncthreads();
+    }
+  };
+  // fragments of this wavefront that hold rows, rounded up to a compiled count
+  const int live = (min(max(nrows - wt * FT * 16, 0), FT * 16) + 15) / 16;
+  if (live > FT / 2)
+    kloop(std::integral_constant<int, FT>{});
+  else if (live > FT / 4)
+    kloop(std::integral_constant<int, FT / 2>{});
+  else if (live > 0)
+    kloop(std::integral_constant<int, (FT / 4 > 0 ? FT / 4 : 1)>{});
+  else
+    kloop(std::integral_constant<int, 0>{});
+
+#pragma unroll
+  for (int t = 0; t < FT; ++t) {
+    const int r = (wt * FT + t) * 16 + nl;
+    if (r >= nrows) continue;
+#pragma unroll
+    for (int f = 0; f < FW; ++f) {
+      const int n = n0 + (ww * FW + f) * 16 + 4 * g;
+      if (n < p.N) store4<F32>(p, grp.begin + r, n, acc[t][f]);
+    }
+  }
+}
+
+template <int F>
+hipError_t launch_stream(const Fp8Gemm& g, hipStream_t st) {
+  const int groups = g.offsets ? std::min(g.rows, g.experts) : 1;
+  const dim3 grid((g.N + 15) / 16, groups), block(64 * kFW);
+  if (g.f32)
+    MOE_LAUNCH((fp8_stream_kernel<F, true>), grid, block, 0, st, g);
+  else
+    MOE_LAUNCH((fp8_stream_kernel<F, false>), grid, block, 0, st, g);
+  return hipGetLastError();
+}
+
+template <int WT, int WW, int FT, int FW>
+hipError_t launch_tile(const Fp8Gemm& g, hipStream_t st) {
+  constexpr int BM = WT * FT * 16, BN = WW * FW * 16;
+  const int nct = (g.N + BN - 1) / BN;
+  int nrt = (g.rows + BM - 1) / BM, grid;
+  if (g.offsets) {
+    nrt = g.rows / BM + std::min(g.rows, g.experts);  // every expert may end in a partial tile
+    grid = xcd_grid(nrt * nct, 2 * nct);
+  } else {
+    grid = (nrt * nct + 7) / 8 * 8;
+  }
+  if (g.f32)
+    MOE_LAUNCH((fp8_tile_kernel<WT, WW, FT, FW, true>), dim3(grid), dim3(64 * WT * WW), 0, st, g, nrt, nct);
+  else
+    MOE_LAUNCH((fp8_tile_kernel<WT, WW, FT, FW, false>), dim3(grid), dim3(64 * WT * WW), 0, st, g, nrt, nct);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t st) {
+  // rows that see one weight row, on average over the experts
+  const int64_t avg = g.offsets ? (static_cast<int64_t>(g.rows) + g.experts - 1) / g.experts : g.rows;
+  if (avg <= 16) return launch_stream<1>(g, st);
+  if (avg <= 32) return launch_stream<2>(g, st);
+  if (avg <= 64) return launch_stream<4>(g, st);
+  return launch_tile<2, 4, 4, 4>(g, st);
+}
+
+}  // namespace moe

@@ -19,6 +19,10 @@ struct StageEvents {
 };
 StageEvents& stage_events();
 
+// The status of a launch: MOE_OK, or MOE_EHIP with the error kept for
+// moe_last_hip_error.
+int report_hip(hipError_t e);
+
 #define MOE_LAUNCH(kern, grid, block, shmem, stream, ...)                                  \
   hipExtLaunchKernelGGL(kern, grid, block, shmem, stream, ::moe::stage_events().start,     \
                         ::moe::stage_events().stop, 0, __VA_ARGS__)

@@ -203,6 +203,7 @@ int need_ptr(P* ptr) {
 
 namespace moe {
 StageEvents& stage_events() { return g_stage_events; }
+int report_hip(hipError_t e) { return hip_status(e); }
 }  // namespace moe
 
 extern "C" {

@@ -1,0 +1,164 @@
+// quant_fp8.hip -- rows to E4M3 codes with one fp32 scale per 128 values,
+// as they are or after SwiGLU (h = silu(gate) * up).
+//
+//   amax = max(2^-90, largest finite |v| of the group)
+//   scale = amax / 448,   code = E4M3(v * (448 / amax)), to nearest, ties to even
+//
+// Both quotients are IEEE fp32 divisions, one each per group; 448 / amax is
+// finite because amax >= 2^-90. A product can exceed 448 by its rounding only,
+// which still rounds to 448. NaN and infinities (a format without infinities)
+// become NaN codes and leave the group's scale to the finite values.
+//
+// Memory bound: each value is read once and held in registers between the
+// maximum and the conversion. A group is one row of 16 lanes with 8 values
+// each (16-byte loads of bf16, 8-byte stores), its maximum four DPP steps.
+#include "device_common.h"
+#include "fp8.h"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr uint32_t kTinyBits = 0x12800000u;  // 2^-90
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// Largest of the 16 lanes of a row, in every lane of it.
+__device__ __forceinline__ uint32_t row16_max_u32(uint32_t v) {
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0xB1, 0xF, 0xF, false)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x4E, 0xF, 0xF, false)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x124, 0xF, 0xF, false)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), 0x128, 0xF, 0xF, false)));
+  return v;
+}
+
+// silu(g) = g / (1 + exp(-g)) through the exponential and reciprocal
+// instructions (1 ulp each): the exponent's rounding error, up to |g| * 2^-24
+// of the result, is taken back by its low part. Beyond +-200 the exponential
+// is 0 or infinite anyway; the bound keeps the low part finite, and below -88,
+// where the exponential may be infinite, it is left out (inf - inf).
+__device__ __forceinline__ float silu(float g) {
+  constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.693147182f;
+  const float b = __builtin_amdgcn_fmed3f(g, -200.0f, 200.0f);
+  const float t = b * kLog2e;
+  const float low = fmaf(b, kLog2eLow, fmaf(b, kLog2e, -t));
+  const float e = __builtin_amdgcn_exp2f(-t);
+  return g * __builtin_amdgcn_rcpf(1.0f + (b > -88.0f ? fmaf(e * kLn2, -low, e) : e));
+}
+
+// Eight consecutive values.
+template <bool F32>
+__device__ __forceinline__ void load8(const void* x, size_t at, float v[8]) {
+  if constexpr (F32) {
+    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
+    const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
+    const uint32_t d[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(d[i] << 16);
+      v[2 * i + 1] = __uint_as_float(d[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+// A workgroup's 16 groups: 2^log_g neighbouring groups of 16 >> log_g rows,
+// and U such sets of rows, their loads issued together.
+template <bool F32, bool SWIGLU, int U>
+__global__ __launch_bounds__(256) void fp8_quant_kernel(Fp8Quant p, int log_g, int nkb) {
+  const int l = threadIdx.x & 15, gi = threadIdx.x >> 4;
+  const int b = (static_cast<int>(blockIdx.y) << log_g) + (gi & ((1 << log_g) - 1));
+  const int rows_per_set = 16 >> log_g;
+  const int row0 = static_cast<int>(blockIdx.x) * (rows_per_set * U) + (gi >> log_g);
+  const int col = b * kFp8Block + l * 8;
+  const bool live_col = col < p.cols;
+  float v[U][8];
+  float up[SWIGLU ? U : 1][8];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int row = row0 + u * rows_per_set;
+    if (live_col && row < p.rows) {
+      const size_t at = static_cast<size_t>(row) * p.ldx + col;
+      load8<F32>(p.x, at, v[u]);
+      if constexpr (SWIGLU) load8<F32>(p.x, at + p.cols, up[u]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[u][i] = 0.0f;
+        if constexpr (SWIGLU) up[u][i] = 0.0f;
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int row = row0 + u * rows_per_set;
+    if constexpr (SWIGLU) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = silu(v[u][i]) * up[u][i];
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[u][i]) & 0x7FFFFFFFu);
+    m = row16_max_u32(m);
+    const bool bad = m >= kInfBits;  // the same in all lanes of the group
+    if (bad) {
+      m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t a = __float_as_uint(v[u][i]) & 0x7FFFFFFFu;
+        if (a < kInfBits) m = max(m, a);
+      }
+      m = row16_max_u32(m);
+    }
+    const float amax = __uint_as_float(max(m, kTinyBits));
+    const float inv = kE4m3Max / amax;
+    if (bad) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if ((__float_as_uint(v[u][i]) & 0x7FFFFFFFu) >= kInfBits) v[u][i] = __uint_as_float(0x7FC00000u);
+    }
+    uint32_t c[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float* q = &v[u][4 * h];
+      int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0] * inv, q[1] * inv, 0, false);
+      w = __builtin_amdgcn_cvt_pk_fp8_f32(q[2] * inv, q[3] * inv, w, true);
+      c[h] = static_cast<uint32_t>(w);
+    }
+    if (live_col && row < p.rows) {
+      *reinterpret_cast<uint2*>(p.codes + static_cast<size_t>(row) * p.cols + col) = uint2{c[0], c[1]};
+      if (l == 0) p.scales[static_cast<size_t>(row) * nkb + b] = amax / kE4m3Max;
+    }
+  }
+}
+
+template <bool F32, bool SWIGLU>
+hipError_t launch_quant(const Fp8Quant& q, hipStream_t st) {
+  const int nkb = fp8_blocks(q.cols);
+  int log_g = 0;
+  while (log_g < 4 && (1 << log_g) < nkb) ++log_g;
+  const int rows_per_set = 16 >> log_g;
+  const unsigned gy = (nkb + (1 << log_g) - 1) >> log_g;
+  constexpr int U = 4;
+  // few rows: one set per workgroup, so that every CU gets some
+  if (static_cast<int64_t>(gy) * ((q.rows + rows_per_set * U - 1) / (rows_per_set * U)) < 512) {
+    const dim3 grid((q.rows + rows_per_set - 1) / rows_per_set, gy);
+    MOE_LAUNCH((fp8_quant_kernel<F32, SWIGLU, 1>), grid, dim3(256), 0, st, q, log_g, nkb);
+  } else {
+    const dim3 grid((q.rows + rows_per_set * U - 1) / (rows_per_set * U), gy);
+    MOE_LAUNCH((fp8_quant_kernel<F32, SWIGLU, U>), grid, dim3(256), 0, st, q, log_g, nkb);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_fp8_quant(const Fp8Quant& q, hipStream_t st) {
+  if (q.swiglu) return q.f32 ? launch_quant<true, true>(q, st) : launch_quant<false, true>(q, st);
+  return q.f32 ? launch_quant<true, false>(q, st) : launch_quant<false, false>(q, st);
+}
+
+}  // namespace moe

@@ -1,0 +1,183 @@
+"""The 8-bit rows, their products and the balance loss without a GPU: the
+argument checks, and the oracle against definitions of its own."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from latent_mixture_experts_amd import binding as B
+from tests import fp8_ref as R
+
+P = 0x10000  # a fake, 16-byte aligned "device" address: never dereferenced
+
+
+def _quant(fn="moe_fp8_quantize", rows=4, cols=256, x=P, ldx=None, t=B.TYPE_BF16, codes=P, scales=P):
+    wide = cols * (2 if "swiglu" in fn else 1)
+    return getattr(B.lib(), fn + "_validate")(rows, cols, x, wide if ldx is None else ldx, t, codes, scales)
+
+
+@pytest.mark.parametrize("fn", ["moe_fp8_quantize", "moe_fp8_swiglu"])
+def test_quantize_arguments(fn):
+    wide = 512 if "swiglu" in fn else 256
+    assert _quant(fn) == B.MOE_OK
+    assert _quant(fn, t=B.TYPE_F32) == B.MOE_OK
+    assert _quant(fn, scales=P + 4) == B.MOE_OK
+    assert _quant(fn, ldx=wide + 8) == B.MOE_OK
+    assert _quant(fn, rows=0, x=None, codes=None, scales=None) == B.MOE_OK
+    for k in ("x", "codes", "scales"):
+        assert _quant(fn, **{k: None}) == B.MOE_EINVAL
+    assert _quant(fn, x=P + 2) == B.MOE_EALIGN
+    assert _quant(fn, codes=P + 8) == B.MOE_EALIGN
+    assert _quant(fn, scales=P + 2) == B.MOE_EALIGN
+    assert _quant(fn, ldx=wide + 4) == B.MOE_EALIGN           # bf16 rows off 16 bytes
+    assert _quant(fn, ldx=wide + 4, t=B.TYPE_F32) == B.MOE_OK  # fp32 rows on them
+    assert _quant(fn, ldx=wide - 8) == B.MOE_EINVAL
+    assert _quant(fn, rows=-1) == B.MOE_EINVAL
+    assert _quant(fn, cols=0) == B.MOE_EINVAL
+    assert _quant(fn, t=2) == B.MOE_EINVAL
+    for cols in (8, 250, 65552):
+        assert _quant(fn, cols=cols) == B.MOE_EUNSUPPORTED
+    assert _quant(fn, cols=2 ** 31 - 16, ldx=2 ** 40) == B.MOE_EUNSUPPORTED
+    assert _quant(fn, ldx=(1 << 22) + 8) == B.MOE_EUNSUPPORTED
+    assert _quant(fn, rows=1 << 28) == B.MOE_EUNSUPPORTED
+
+
+def _linear(T=4, N=256, K=512, x=P, ldx=None, xs=P, w=P, ws=P, out=P, ldo=None, t=B.TYPE_BF16):
+    return B.lib().moe_fp8_linear_validate(T, N, K, x, K if ldx is None else ldx, xs, w, ws, out,
+                                           N if ldo is None else ldo, t)
+
+
+def _grouped(rows=4, E=8, N=256, K=512, off=P, idx=None, div=1, x_rows=None, x=P, ldx=None, xs=P, w=P,
+             ws=P, out=P, ldo=None, t=B.TYPE_BF16):
+    return B.lib().moe_fp8_grouped_validate(rows, E, N, K, off, idx, div, rows if x_rows is None else x_rows,
+                                            x, K if ldx is None else ldx, xs, w, ws, out,
+                                            N if ldo is None else ldo, t)
+
+
+@pytest.mark.parametrize("fn", [_linear, _grouped])
+def test_product_arguments(fn):
+    rows = "T" if fn is _linear else "rows"
+    assert fn() == B.MOE_OK
+    assert fn(t=B.TYPE_F32, N=7, K=16) == B.MOE_OK
+    assert fn(xs=P + 4, ws=P + 8, out=P + 2) == B.MOE_OK
+    assert fn(out=P + 2, t=B.TYPE_F32) == B.MOE_EALIGN
+    assert fn(**{rows: 0}, x=None, xs=None, w=None, ws=None, out=None) == B.MOE_OK
+    for k in ("x", "xs", "w", "ws", "out"):
+        assert fn(**{k: None}) == B.MOE_EINVAL
+    assert fn(x=P + 8) == B.MOE_EALIGN
+    assert fn(w=P + 4) == B.MOE_EALIGN
+    assert fn(xs=P + 2) == B.MOE_EALIGN
+    assert fn(ldx=520) == B.MOE_EALIGN
+    assert fn(ldx=496) == B.MOE_EINVAL
+    assert fn(ldo=255) == B.MOE_EINVAL
+    assert fn(ldo=257) == B.MOE_OK
+    assert fn(t=-1) == B.MOE_EINVAL
+    for bad in (dict(N=0), dict(K=0), {rows: -1}):
+        assert fn(**bad) == B.MOE_EINVAL
+    for big in (dict(K=520), dict(K=65552), dict(N=65537), {rows: 1 << 28}, dict(ldx=(1 << 22) + 16),
+                dict(ldo=(1 << 22) + 1)):
+        assert fn(**big) == B.MOE_EUNSUPPORTED, big
+
+
+def test_grouped_arguments():
+    assert _grouped(E=0) == B.MOE_EINVAL
+    assert _grouped(E=257) == B.MOE_EUNSUPPORTED
+    assert _grouped(off=None) == B.MOE_EINVAL
+    assert _grouped(off=P + 2) == B.MOE_EALIGN
+    assert _grouped(x_rows=3) == B.MOE_EINVAL               # fewer rows than the outputs, no index
+    assert _grouped(x_rows=1, idx=P) == B.MOE_OK
+    assert _grouped(x_rows=1, idx=P, div=8) == B.MOE_OK
+    assert _grouped(x_rows=0, idx=P) == B.MOE_EINVAL
+    assert _grouped(idx=P + 2) == B.MOE_EALIGN
+    assert _grouped(idx=P, div=0) == B.MOE_EINVAL
+    assert _grouped(div=2) == B.MOE_EINVAL                  # a divisor without an index
+    assert _grouped(x_rows=-1) == B.MOE_EINVAL
+    assert _grouped(idx=P, x_rows=(1 << 31) // 512) == B.MOE_EUNSUPPORTED
+    assert _grouped(idx=P, x_rows=(1 << 31) // 512 - 1) == B.MOE_OK
+
+
+def _loss(T=100, E=16, K=4, logits=P, ids=P, mask=None, counts=P, losses=P, ws=P, nbytes=1 << 30):
+    return B.lib().moe_balance_loss_validate(T, E, K, logits, ids, mask, counts, losses, ws, nbytes)
+
+
+def _back(T=100, E=16, K=4, logits=P, ids=P, mask=None, counts=P, gl=P, w=P, dw=P, out=P):
+    return B.lib().moe_balance_loss_backward_validate(T, E, K, logits, ids, mask, counts, gl, w, dw, out)
+
+
+def test_balance_arguments():
+    assert _loss() == B.MOE_OK and _back() == B.MOE_OK
+    assert _loss(mask=P + 1) == B.MOE_OK and _back(mask=P + 3) == B.MOE_OK
+    assert B.balance_workspace_bytes(64, 256) == 0
+    need = B.balance_workspace_bytes(100, 16)
+    assert need > 0
+    assert _loss(nbytes=need) == B.MOE_OK
+    assert _loss(nbytes=need - 1) == B.MOE_EWORKSPACE
+    assert _loss(ws=None, nbytes=0) == B.MOE_EINVAL
+    assert _loss(T=64, ws=None, nbytes=0) == B.MOE_OK
+    assert _loss(T=0, logits=None, ids=None, ws=None, nbytes=0) == B.MOE_OK
+    for k in ("logits", "ids", "counts", "losses"):
+        assert _loss(**{k: None}) == B.MOE_EINVAL
+    assert _loss(logits=P + 4) == B.MOE_EALIGN
+    assert _loss(ids=P + 2) == B.MOE_EALIGN
+    for k in ("logits", "counts", "gl", "out"):
+        assert _back(**{k: None}) == B.MOE_EINVAL
+    assert _back(T=0, logits=None, counts=None, gl=None, out=None, w=None, dw=None) == B.MOE_OK
+    assert _back(w=None) == B.MOE_EINVAL and _back(dw=None) == B.MOE_EINVAL
+    assert _back(w=None, dw=None, ids=None) == B.MOE_OK
+    assert _back(ids=None) == B.MOE_EINVAL
+    assert _back(out=P + 8) == B.MOE_EALIGN
+    for fn in (_loss, _back):
+        assert fn(T=-1) == B.MOE_EINVAL
+        assert fn(E=0) == B.MOE_EINVAL
+        assert fn(K=0) == B.MOE_EINVAL
+        assert fn(E=257) == B.MOE_EUNSUPPORTED
+        assert fn(K=9) == B.MOE_EUNSUPPORTED
+        assert fn(E=2, K=3) == B.MOE_EUNSUPPORTED
+        assert fn(T=1 << 28) == B.MOE_EUNSUPPORTED
+    assert B.balance_workspace_bytes(-1, 16) == 0 and B.balance_workspace_bytes(100, 257) == 0
+
+
+def test_host_tensors_are_refused():
+    x = torch.zeros((4, 128), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        B.fp8_quantize(x)
+    with pytest.raises(ValueError):
+        B.balance_loss(torch.zeros((4, 8)), torch.zeros((4, 2), dtype=torch.int32))
+
+
+def test_oracle_rounds_to_e4m3():
+    """Every representable value maps to itself, and what lies between two to the nearer (ties to even)."""
+    v = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    v = v[torch.isfinite(v)]
+    assert torch.equal(R.e4m3(v), v)
+    s = torch.unique(v)
+    mid = (s[1:] + s[:-1]) / 2
+    got = R.e4m3(torch.stack([mid - 1e-9, mid, mid + 1e-9]))
+    assert torch.equal(got[0], s[:-1]) and torch.equal(got[2], s[1:])
+    assert torch.equal(got[1], mid.float().to(torch.float8_e4m3fn).double())
+
+
+def test_oracle_gradient_against_differences():
+    """The balance gradient against central differences of the losses with f
+    held, and the gating part against the softmax of the selected logits."""
+    g = torch.Generator().manual_seed(3)
+    t, e, k = 5, 7, 3
+    lg = torch.randn((t, e), generator=g, dtype=torch.float64)
+    ids = lg.topk(k, 1).indices.to(torch.int32)
+    mask = torch.tensor([1, 0, 1, 1, 1])
+    dw = torch.randn((t, k), generator=g, dtype=torch.float64)
+    gl = torch.tensor([0.7, 0.3])
+
+    def total(x):
+        w = torch.softmax(torch.gather(x, 1, ids.long()), 1)
+        losses, _, _, _ = R.balance(x, ids, mask)
+        return (losses * gl).sum() + (w * dw * mask[:, None]).sum()
+
+    w = torch.softmax(torch.gather(lg, 1, ids.long()), 1)
+    grad = R.balance(lg, ids, mask, gl, w, dw)[2]
+    for i in range(t):
+        for j in range(e):
+            d = torch.zeros_like(lg)
+            d[i, j] = 1e-5
+            diff = (total(lg + d) - total(lg - d)) / 2e-5
+            assert abs(float(diff - grad[i, j])) < 1e-8  # (1e-10 of third derivatives, 1e-16 / 1e-5 of rounding)

@@ -1,0 +1,224 @@
+"""The balance loss, the routes per expert and the gradient of the router
+logits on the GPU against 64 bits (tests/fp8_ref.py)."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from tests import fp8_ref as R
+
+pytestmark = pytest.mark.gpu
+B = pytest.importorskip("latent_mixture_experts_amd.binding")
+INF = float("inf")
+
+
+def case(T, E, K, masked, seed=0, spread=2.0):
+    g = torch.Generator().manual_seed(seed + T + E)
+    logits = torch.randn((T, E), generator=g) * spread + torch.randn((1, E), generator=g)
+    best = logits.topk(K, 1)
+    ids, w = best.indices.to(torch.int32), torch.softmax(best.values, 1)
+    dw = torch.randn((T, K), generator=g)
+    mask = (torch.rand(T, generator=g) < 0.8).to(torch.uint8) if masked else None
+    return logits, ids, w, dw, mask
+
+
+def cuda(t):
+    return None if t is None else t.cuda()
+
+
+def check_loss(losses, counts, ref, ref_c):
+    assert counts.cpu().tolist() == ref_c.tolist()
+    # probabilities: exponential and quotient under 8 half steps; sums of positive terms: at most
+    # 64 tokens of a row, 16 rows, 128 + 4 joins; f, the products and the sum over the experts 16 more
+    rel = (8 + 64 + 16 + 132 + 16) * R.U24
+    got = losses.cpu().double()
+    assert abs(float(got[0] - ref[0])) <= rel * float(ref[0]) + 1e-30
+    # lse^2: the logarithm's own error is absolute, a few steps of the sizes of maximum and logarithm
+    assert abs(float(got[1] - ref[1])) <= 2 * rel * float(ref[1]) + 1e-12
+
+
+def check_grad(got, ref, size):
+    # per entry: expf, logf, the quotients and the two 256-term sums (16 in a lane, four joins): under 64 half steps
+    err = (got.cpu().double() - ref).abs()
+    assert bool((err <= 64 * R.U24 * size + 1e-30).all()), float((err / (size + 1e-30)).max() / R.U24)
+
+
+SHAPES = [(1, 1, 1), (1, 256, 8), (3, 5, 2), (16, 16, 4), (61, 16, 4), (64, 255, 8), (65, 64, 1), (100, 3, 3),
+          (333, 130, 7), (1000, 256, 8), (9001, 256, 8), (20000, 12, 2), (40000, 66, 6)]
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("T,E,K", SHAPES)
+def test_loss_and_gradient(T, E, K, masked):
+    logits, ids, w, dw, mask = case(T, E, K, masked)
+    gl = torch.tensor([0.7, 0.02])
+    ref, ref_c, grad, size = R.balance(logits, ids, mask, gl, w, dw)
+    losses, counts = B.balance_loss(logits.cuda(), ids.cuda(), cuda(mask))
+    check_loss(losses, counts, ref, ref_c)
+    got = B.balance_loss_backward(logits.cuda(), ids.cuda(), counts, gl.cuda(), cuda(mask), w.cuda(), dw.cuda())
+    check_grad(got, grad, size)
+    grad, size = R.balance(logits, ids, mask, gl)[2:]
+    got = B.balance_loss_backward(logits.cuda(), ids.cuda(), counts, gl.cuda(), cuda(mask))
+    check_grad(got, grad, size)
+
+
+@pytest.mark.parametrize("T", [50, 300])
+def test_tokens_that_do_not_count(T):
+    """Masked tokens may hold anything; tokens whose logits are all -inf do
+    not count; -inf for some experts is a probability of zero."""
+    logits, ids, w, dw, mask = case(T, 20, 4, True)
+    logits[mask == 0] = float("nan")
+    logits[3, :], mask[3] = -INF, 1
+    logits[7, 5:], mask[7] = -INF, 1
+    logits[9, :], mask[9] = torch.finfo(torch.float32).min, 1
+    logits[11, :], mask[11] = 3e38, 1  # (lse^2 overflows: left to the balance loss alone)
+    gl = torch.tensor([1.0, 0.0])
+    ref, ref_c, grad, size = R.balance(logits, ids, mask, gl, w, dw)
+    losses, counts = B.balance_loss(logits.cuda(), ids.cuda(), mask.cuda())
+    assert counts.cpu().tolist() == ref_c.tolist()
+    assert abs(float(losses[0].cpu().double() - ref[0])) <= 300 * R.U24 * float(ref[0])
+    got = B.balance_loss_backward(logits.cuda(), ids.cuda(), counts, gl.cuda(), mask.cuda(), w.cuda(), dw.cuda())
+    assert bool((got.cpu()[mask == 0] == 0).all()) and bool((got.cpu()[3] == 0).all())
+    check_grad(got, grad, size)
+
+
+@pytest.mark.parametrize("T", [0, 5, 200])
+def test_nothing_counts(T):
+    logits, ids, w, dw, _ = case(max(T, 1), 12, 3, False)
+    logits, ids, w, dw = logits[:T], ids[:T], w[:T], dw[:T]
+    mask = torch.zeros(T, dtype=torch.bool, device="cuda")
+    losses, counts = B.balance_loss(logits.cuda(), ids.cuda(), mask)
+    assert losses.tolist() == [0.0, 0.0] and counts.tolist() == [0] * 13
+    got = B.balance_loss_backward(logits.cuda(), ids.cuda(), counts, torch.ones(2, device="cuda"), mask, w.cuda(),
+                                  dw.cuda())
+    assert got.shape == (T, 12) and bool((got == 0).all())
+
+
+def test_nan_and_inf_logits_show():
+    logits, ids, w, dw, _ = case(70, 8, 2, False)
+    logits[4, 2] = float("nan")
+    losses, counts = B.balance_loss(logits.cuda(), ids.cuda())
+    assert torch.isnan(losses).all() and int(counts[8]) == 70
+    got = B.balance_loss_backward(logits.cuda(), ids.cuda(), counts, torch.ones(2, device="cuda"))
+    assert torch.isnan(got[4]).all() and torch.isfinite(torch.cat([got[:4], got[5:]])).all()
+
+
+def test_repeated_and_foreign_ids():
+    """An expert listed twice counts and adds twice; ids outside the experts neither count nor add."""
+    logits, ids, w, dw, _ = case(90, 10, 4, False)
+    ids[5] = torch.tensor([2, 2, 7, 2], dtype=torch.int32)
+    ids[6] = torch.tensor([-1, 10, 3, 2 ** 31 - 1], dtype=torch.int32)
+    gl = torch.tensor([0.5, 0.1])
+    ref, ref_c, grad, size = R.balance(logits, ids, None, gl, w, dw)
+    losses, counts = B.balance_loss(logits.cuda(), ids.cuda())
+    check_loss(losses, counts, ref, ref_c)
+    got = B.balance_loss_backward(logits.cuda(), ids.cuda(), counts, gl.cuda(), None, w.cuda(), dw.cuda())
+    check_grad(got, grad, size)
+
+
+def test_even_routing_gives_one():
+    T, E, K = 96, 12, 3
+    logits = torch.zeros((T, E), device="cuda")
+    ids = ((torch.arange(T)[:, None] * K + torch.arange(K)) % E).to(torch.int32).cuda()
+    losses, counts = B.balance_loss(logits, ids)
+    assert counts.tolist() == [T * K // E] * E + [T]
+    assert abs(float(losses[0]) - 1.0) < 300 * R.U24
+
+
+def test_counts_of_the_whole_batch():
+    """Two halves with summed counts give the whole batch's gradient (per half: N is the batch's)."""
+    logits, ids, w, dw, mask = case(500, 40, 4, True)
+    gl = torch.tensor([0.3, 0.1])
+    _, _, grad, size = R.balance(logits, ids, mask, gl, w, dw)
+    parts = [(logits[:200], ids[:200], w[:200], dw[:200], mask[:200]), (logits[200:], ids[200:], w[200:], dw[200:], mask[200:])]
+    counts = sum(B.balance_loss(l.cuda(), i.cuda(), m.cuda())[1] for l, i, _, _, m in parts)
+    got = torch.cat([B.balance_loss_backward(l.cuda(), i.cuda(), counts, gl.cuda(), m.cuda(), a.cuda(), b.cuda())
+                     for l, i, a, b, m in parts])
+    check_grad(got, grad, size)
+
+
+def test_gradient_against_differences():
+    """Central differences of the GPU's own losses. Step h = 2^-4 of a logit:
+    the third derivatives of both losses in one logit are at most 8 f_max / N
+    and 16 (1 + lse) / N, so h^2 / 6 of those; and 64 half steps of the loss over 2h."""
+    T, E, K = 6, 5, 2
+    logits, ids, _, _, _ = case(T, E, K, False, spread=1.0)
+    h = 2.0 ** -4
+    losses, counts = B.balance_loss(logits.cuda(), ids.cuda())
+    f_max = float((counts[:E].double() * E / (K * T)).max())
+    lse = float(torch.logsumexp(logits.double(), 1).abs().max())
+    for which, third in ((0, 8 * f_max / T), (1, 16 * (1 + lse) / T)):
+        gl = torch.zeros(2)
+        gl[which] = 1.0
+        grad = B.balance_loss_backward(logits.cuda(), ids.cuda(), counts, gl.cuda()).cpu().double()
+        bound = h * h / 6 * third + 64 * R.U24 * float(losses[which]) / h
+        for t in range(T):
+            for e in range(E):
+                d = torch.zeros_like(logits)
+                d[t, e] = h
+                up = B.balance_loss((logits + d).cuda(), ids.cuda())[0]
+                dn = B.balance_loss((logits - d).cuda(), ids.cuda())[0]
+                diff = float(up[which].double() - dn[which].double()) / (2 * h)
+                assert abs(diff - float(grad[t, e])) <= bound, (which, t, e, diff, float(grad[t, e]), bound)
+
+
+@pytest.mark.parametrize("T", [40, 5000])
+def test_captured_and_deterministic(T):
+    logits, ids, w, dw, mask = (cuda(t) for t in case(T, 256, 8, True))
+    gl = torch.tensor([0.3, 0.1], device="cuda")
+    ws = torch.empty(max(B.balance_workspace_bytes(T, 256), 16), dtype=torch.uint8, device="cuda")
+
+    def run():
+        losses, counts = B.balance_loss(logits, ids, mask, ws)
+        return losses, counts, B.balance_loss_backward(logits, ids, counts, gl, mask, w, dw)
+
+    first = run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for seed in range(4):
+        if seed:
+            logits.add_(torch.randn(logits.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(seed)))
+        ws.fill_(255)  # (what the workspace held does not matter)
+        graph.replay()
+        got = [t.clone() for t in out]
+        want = run()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), seed
+        if seed == 0:
+            assert all(torch.equal(a, b) for a, b in zip(got, first))
+
+
+def test_loss_from_the_router():
+    """moe_route's logits, ids and offsets: the counts are the offsets' steps."""
+    dims = dict(hidden=256, latent=128, inter=128, n_experts=24, top_k=3)
+    g = torch.Generator().manual_seed(8)
+    x = torch.randn((150, 256), generator=g).bfloat16().cuda()
+    router = (torch.randn((24, 256), generator=g) * 0.1).cuda()
+    d = B.make_dims(dims)
+    r = B.route(d, x.view(torch.int16), router, B.alloc_workspace(d, 150))
+    losses, counts = B.balance_loss(r["logits"], r["ids"])
+    assert torch.equal(counts[:24], r["offsets"][1:] - r["offsets"][:-1]) and int(counts[24]) == 150
+    gl, dw = torch.tensor([0.1, 0.01]), torch.randn((150, 3), generator=g)
+    ref, ref_c, grad, size = R.balance(r["logits"].cpu(), r["ids"].cpu(), None, gl, r["w"].cpu(), dw)
+    check_loss(losses, counts, ref, ref_c)
+    got = B.balance_loss_backward(r["logits"], r["ids"], counts, gl.cuda(), None, r["w"], dw.cuda())
+    check_grad(got, grad, size)
+
+
+def test_refusals():
+    logits, ids, w, dw, mask = (cuda(t) for t in case(70, 8, 2, True))
+    counts = torch.zeros(9, dtype=torch.int32, device="cuda")
+    gl = torch.ones(2, device="cuda")
+    for bad in (lambda: B.balance_loss(logits.double(), ids), lambda: B.balance_loss(logits, ids.long()),
+                lambda: B.balance_loss(logits, ids[:60]), lambda: B.balance_loss(logits.t(), ids),
+                lambda: B.balance_loss(logits, ids, mask[:60]), lambda: B.balance_loss(logits, ids, mask.float()),
+                lambda: B.balance_loss_backward(logits, ids, counts[:8], gl),
+                lambda: B.balance_loss_backward(logits, ids, counts, gl, w=w),
+                lambda: B.balance_loss_backward(logits, ids, counts, gl.cpu()),
+                lambda: B.balance_loss_backward(logits, ids, counts, gl, w=w, grad_w=dw[:, :1])):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(B.MoeError) as e:
+        B.balance_loss(logits, ids, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == B.MOE_EWORKSPACE

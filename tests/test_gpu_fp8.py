@@ -1,0 +1,432 @@
+"""The 8-bit rows and their products on the GPU against 64-bit definitions
+(tests/fp8_ref.py): group edges, ragged widths, few and many rows, empty
+experts, strides, gathers, NaN and infinities, streams, graphs."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from tests import fp8_ref as R
+
+pytestmark = pytest.mark.gpu
+B = pytest.importorskip("latent_mixture_experts_amd.binding")
+F8 = torch.float8_e4m3fn
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def activations(rows, cols, g, dtype):
+    x = torch.randn((rows, cols), generator=g) * torch.exp(2 * torch.randn((rows, 1), generator=g))
+    return x.to(dtype)
+
+
+# ---- quantisation ----------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(1, 16), (1, 8192), (3, 112), (5, 128), (17, 144), (64, 272), (33, 4096),
+                                       (1000, 2064), (2500, 640)])
+def test_quantize_is_the_stated_arithmetic(rows, cols, dtype):
+    x = activations(rows, cols, gen(rows + cols), dtype)
+    codes, scales = B.fp8_quantize(x.cuda())
+    ref, ref_s = R.quantize_f32(x.float())
+    assert torch.equal(scales.cpu(), ref_s)
+    assert torch.equal(R.canonical(codes.cpu().view(torch.uint8)), ref)
+    # and against 64 bits: half a step of E4M3 at the value, and the two fp32 quotients' roundings
+    v, s = x.double(), R.expand(scales.cpu(), cols)
+    q = (v / s).abs().clamp_min(2.0 ** -6)
+    half = torch.exp2(torch.floor(torch.log2(q)) - 4)
+    back = codes.cpu().double() * s
+    assert bool(((back - v).abs() <= s * (half * (1 + 8 * R.U24) + q * 8 * R.U24)).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantize_special_values(dtype):
+    inf, nan = float("inf"), float("nan")
+    x = torch.zeros((9, 256))
+    x[0, 3] = 1.0                       # one value, the rest zero
+    x[1, :] = torch.linspace(-1, 1, 256)
+    x[1, 5], x[1, 200] = inf, nan       # non-finite values among finite ones, one per group
+    x[2, :] = nan
+    x[3, :128], x[3, 128:] = -inf, inf
+    x[4, :] = 2.0 ** -126               # below the smallest scale
+    x[4, 128] = 2.0 ** -89
+    x[5, :] = torch.finfo(dtype).max
+    x[6, :] = torch.where(torch.arange(256) % 2 == 0, 448.0, 27.0)  # exact codes and ties
+    x[7, :] = -0.0
+    x[8, :] = torch.finfo(torch.bfloat16).tiny / 8                 # a denormal
+    x = x.to(dtype)
+    codes, scales = B.fp8_quantize(x.cuda())
+    ref, ref_s = R.quantize_f32(x.float())
+    assert torch.equal(scales.cpu(), ref_s)
+    assert torch.isfinite(scales).all()
+    assert torch.equal(R.canonical(codes.cpu().view(torch.uint8)), ref)
+
+
+def test_quantize_strided_rows_and_given_outputs():
+    g = gen(5)
+    wide = activations(40, 1024, g, torch.bfloat16).cuda()
+    x = wide[:, 256:512]
+    codes = torch.empty((40, 256), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((40, 2), device="cuda")
+    B.fp8_quantize(x, codes, scales)
+    ref, ref_s = R.quantize_f32(x.float().cpu())
+    assert torch.equal(R.canonical(codes.cpu()), ref) and torch.equal(scales.cpu(), ref_s)
+    bits = B.fp8_quantize(x.contiguous().view(torch.int16))  # bf16 as bit patterns
+    assert torch.equal(bits[0].view(torch.uint8), codes)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,inter", [(1, 16), (7, 144), (300, 512), (1100, 4096)])
+def test_swiglu(rows, inter, dtype):
+    g = gen(rows)
+    gu = torch.randn((rows, 2 * inter), generator=g) * 3
+    gu[0, :8] = torch.tensor([-100.0, -90.0, -50.0, -20.0, 20.0, 90.0, 300.0, -300.0])
+    gu = gu.to(dtype)
+    codes, scales = B.fp8_swiglu(gu.cuda())
+    d = gu.double()
+    h = d[:, :inter] * torch.sigmoid(d[:, :inter]) * d[:, inter:]
+    amax = R.groups(h).abs().amax(2).clamp_min(R.TINY)
+    # exponential and reciprocal 1 ulp each, the low part's 1, five roundings: under 16 half steps
+    rel = 16 * R.U24
+    assert bool(((scales.cpu().double() - amax / 448).abs() <= (rel + 2 * R.U24) * amax / 448).all())
+    s = R.expand(scales.cpu(), inter)
+    q = (h / s).abs().clamp_min(2.0 ** -6)
+    half = torch.exp2(torch.floor(torch.log2(q * (1 + 2 * rel))) - 4)
+    back = codes.cpu().double() * s
+    # (2^-126 / 448: what a flushed denormal product may lose)
+    assert bool(((back - h).abs() <= s * (half + q * (2 * rel)) + 2.0 ** -126).all())
+
+
+def test_swiglu_of_far_gates():
+    """Every gate down to the exponential's overflow and far beyond it is finite, and zero there."""
+    gate = torch.cat([torch.linspace(-210, -80, 4000), torch.tensor([-1e4, -1e30, -3e38]), torch.zeros(93)])
+    up = torch.full_like(gate, -2.0)
+    codes, scales = B.fp8_swiglu(torch.cat([gate, up])[None].cuda())
+    back = codes.cpu().float() * R.expand(scales.cpu(), gate.numel()).float()
+    assert torch.isfinite(back).all() and torch.isfinite(scales).all()
+    assert float(back.abs().max()) < 2.0 ** -90
+
+
+def test_swiglu_non_finite():
+    gu = torch.ones((4, 256))
+    gu[0, 3] = float("nan")
+    gu[1, 4] = float("inf")
+    gu[2, 5] = -float("inf")
+    gu[3, 128 + 6] = float("nan")
+    codes, scales = B.fp8_swiglu(gu.cuda())
+    c = codes.cpu().float()
+    for r, j in ((0, 3), (1, 4), (2, 5), (3, 6)):
+        assert torch.isnan(c[r, j]) and int(torch.isnan(c[r]).sum()) == 1
+    assert torch.isfinite(scales).all()
+
+
+def test_zero_rows():
+    x = torch.empty((0, 256), dtype=torch.bfloat16, device="cuda")
+    codes, scales = B.fp8_quantize(x)
+    assert codes.shape == (0, 256) and scales.shape == (0, 2)
+    w, ws = torch.zeros((64, 256), dtype=F8, device="cuda"), torch.ones((1, 2), device="cuda")
+    assert B.fp8_linear(codes, scales, w, ws).shape == (0, 64)
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    out = B.fp8_grouped(codes, scales, off, w.repeat(2, 1).view(2, 64, 256), ws.repeat(2, 1).view(2, 1, 2))
+    assert out.shape == (0, 64)
+
+
+# ---- products --------------------------------------------------------------
+
+def operands(rows, n, k, g, experts=None):
+    x, xs = R.random_codes((rows, k), g), R.random_scales((rows, R.blocks(k)), g)
+    lead = () if experts is None else (experts,)
+    w, ws = R.random_codes((*lead, n, k), g), R.random_scales((*lead, R.blocks(n), R.blocks(k)), g)
+    return x, xs, w, ws
+
+
+def dev(*ts):
+    return [t.cuda() for t in ts]
+
+
+SHAPES = [(1, 1, 16), (1, 256, 128), (1, 4096, 1024), (2, 130, 144), (15, 16, 8192), (16, 127, 112), (17, 129, 256),
+          (31, 64, 4112), (33, 272, 640), (64, 128, 128), (65, 128, 1024), (100, 1, 32), (127, 7, 528),
+          (128, 256, 512), (129, 257, 640), (257, 384, 1040), (500, 1000, 272), (700, 255, 2048)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,n,k", SHAPES)
+def test_linear(rows, n, k, dtype):
+    x, xs, w, ws = operands(rows, n, k, gen(rows * 7 + n + k))
+    got = B.fp8_linear(*dev(x, xs, w, ws), dtype)
+    assert got.dtype == dtype and got.shape == (rows, n)
+    R.assert_product(got.cpu(), x, xs, w, ws)
+
+
+@pytest.mark.parametrize("rows", [1, 20, 40, 150])
+def test_every_position_counts_once(rows):
+    """One nonzero code per row of x and every code value in w: out is that code times the scales."""
+    k, n = 512, 300
+    g = gen(rows)
+    at = torch.randint(0, k, (rows,), generator=g)
+    x = torch.zeros((rows, k), dtype=torch.uint8)
+    x[torch.arange(rows), at] = 0x38  # 1.0
+    w = torch.randint(0, 256, (n, k), generator=g, dtype=torch.uint8)
+    w[w & 0x7F == 0x7F] = 0
+    xs = torch.exp2(torch.randint(-3, 4, (rows, 4), generator=g).float())
+    ws = torch.exp2(torch.randint(-3, 4, (3, 4), generator=g).float())
+    got = B.fp8_linear(*dev(x, xs, w, ws), torch.float32).cpu()
+    wd = w.view(F8).float() * R.expand(ws, k).float().repeat_interleave(128, 0)[:n]
+    assert torch.equal(got, (wd[:, at] * xs[torch.arange(rows), at // 128]).t())
+
+
+@pytest.mark.parametrize("rows", [3, 24, 50, 200])
+def test_nan_codes_stay_in_their_row_and_column(rows):
+    x, xs, w, ws = operands(rows, 200, 384, gen(rows))
+    xb, wb = x.view(torch.uint8), w.view(torch.uint8)
+    xb[1, 380] = 0x7F
+    wb[150, 3] = 0xFF
+    got = B.fp8_linear(*dev(x, xs, w, ws), torch.float32).cpu()
+    want = torch.zeros((rows, 200), dtype=torch.bool)
+    want[1, :], want[:, 150] = True, True
+    assert torch.equal(torch.isnan(got), want)
+
+
+@pytest.mark.parametrize("rows", [5, 40, 300])
+def test_linear_strides(rows):
+    """Rows of x in a wider buffer, out a slice of a wider one whose other columns stay."""
+    g = gen(rows)
+    n, k = 200, 400
+    wide = R.random_codes((rows, 1024), g)
+    _, xs, w, ws = operands(rows, n, k, g)
+    x = wide.cuda()[:, 512:512 + k]
+    for dtype in (torch.bfloat16, torch.float32):
+        for lo, total in ((0, 200), (3, 331), (8, 256)):
+            buf = torch.full((rows, total), 7.0, dtype=dtype, device="cuda")
+            B.fp8_linear(x, *dev(xs, w, ws), out=buf[:, lo:lo + n])
+            R.assert_product(buf[:, lo:lo + n].cpu(), wide[:, 512:512 + k], xs, w, ws, (dtype, lo))
+            rest = torch.cat([buf[:, :lo], buf[:, lo + n:]], 1)
+            assert bool((rest == 7.0).all())
+
+
+def sizes_case(name, experts, g):
+    if name == "uniform":
+        return [5] * experts
+    if name == "one expert":
+        return [0] * (experts - 1) + [90]
+    if name == "edges":
+        return ([0, 1, 15, 16, 17, 0, 63, 64, 65, 127, 128, 129, 0, 250] * experts)[:experts]
+    if name == "many":
+        return torch.randint(90, 180, (experts,), generator=g).tolist()
+    if name == "first only":
+        return [3] + [0] * (experts - 1)
+    return torch.randint(0, 4, (experts,), generator=g).tolist()
+
+
+def check_grouped(got, x, xs, w, ws, bounds, rows_of=None):
+    for e, (a, b) in enumerate(zip(bounds, bounds[1:])):
+        if b > a:
+            at = torch.arange(a, b) if rows_of is None else rows_of[a:b]
+            R.assert_product(got[a:b], x[at], xs[at], w[e], ws[e], e)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("name,experts,n,k", [
+    ("uniform", 6, 128, 256), ("one expert", 9, 144, 400), ("edges", 14, 272, 384), ("edges", 28, 33, 144),
+    ("many", 5, 300, 640), ("first only", 256, 64, 128), ("few", 256, 48, 272), ("few", 255, 130, 128),
+    ("edges", 3, 512, 2048), ("many", 1, 257, 1040)])
+def test_grouped(name, experts, n, k, dtype):
+    g = gen(experts + n)
+    sizes = sizes_case(name, experts, g)
+    bounds = [0] + torch.tensor(sizes).cumsum(0).tolist()
+    rows = bounds[-1]
+    x, xs, w, ws = operands(rows, n, k, g, experts)
+    off = torch.tensor(bounds, dtype=torch.int32)
+    got = B.fp8_grouped(*dev(x, xs, off, w, ws), dtype)
+    check_grouped(got.cpu(), x, xs, w, ws, bounds)
+
+
+@pytest.mark.parametrize("rows_per", [2, 30, 60, 200])
+def test_grouped_gather_and_rows_outside(rows_per):
+    """Rows read through an index with a divisor, out of range ones clamped;
+    output rows before the first and behind the last expert's stay as they were."""
+    g = gen(rows_per)
+    experts, n, k, top = 4, 272, 400, 3
+    sizes = [rows_per, 0, rows_per + 5, 1]
+    bounds = [4] + (4 + torch.tensor(sizes).cumsum(0)).tolist()
+    rows, x_rows = bounds[-1] + 9, 37
+    x, xs, w, ws = operands(x_rows, n, k, g, experts)
+    index = torch.randint(0, x_rows * top, (rows,), generator=g, dtype=torch.int32)
+    index[5], index[6] = x_rows * top + 100, -50
+    out = torch.full((rows, n), 3.0, device="cuda")
+    B.fp8_grouped(*dev(x, xs, torch.tensor(bounds, dtype=torch.int32), w, ws), row_index=index.cuda(), index_div=top,
+                  out=out)
+    got = out.cpu()
+    assert bool((got[:4] == 3.0).all()) and bool((got[bounds[-1]:] == 3.0).all())
+    src = torch.div(index, top, rounding_mode="trunc").clamp(0, x_rows - 1).long()
+    check_grouped(got, x, xs, w, ws, bounds, src)
+
+
+def test_grouped_repeated_index_and_strides():
+    g = gen(11)
+    x, xs, w, ws = operands(6, 96, 128, g, 2)
+    wide = torch.zeros((6, 256), dtype=torch.uint8)
+    wide[:, 64:192] = x.view(torch.uint8)
+    index = torch.tensor([2, 2, 2, 5, 0, 2], dtype=torch.int32)
+    bounds = [0, 4, 6]
+    buf = torch.zeros((6, 131), device="cuda")
+    B.fp8_grouped(wide.cuda()[:, 64:192], xs.cuda(), torch.tensor(bounds, dtype=torch.int32).cuda(), *dev(w, ws),
+                  row_index=index.cuda(), out=buf[:, 5:101])
+    check_grouped(buf[:, 5:101].cpu(), x, xs, w, ws, bounds, index.long())
+    assert float(buf[:, :5].abs().sum() + buf[:, 101:].abs().sum()) == 0.0
+
+
+@pytest.mark.parametrize("rows", [1, 40, 300])
+def test_bad_offsets_stay_inside(rows):
+    """Offsets that decrease or leave the rows: nothing outside out is written, no error."""
+    x, xs, w, ws = operands(rows, 144, 128, gen(rows), 3)
+    guard = torch.full((rows + 64, 144), 5.0, device="cuda")
+    for off in ([0, rows + 40, 2 * rows, 3 * rows], [rows, 0, rows, 0], [-7, rows, -100, rows],
+                [2 ** 31 - 1, -2 ** 31, 0, 2 ** 31 - 1]):
+        B.fp8_grouped(*dev(x, xs, torch.tensor(off, dtype=torch.int32), w, ws), out=guard[32:32 + rows])
+        assert bool((guard[:32] == 5.0).all()) and bool((guard[32 + rows:] == 5.0).all())
+
+
+@pytest.mark.parametrize("rows", [1, 30, 60, 400])
+def test_same_bits_every_time(rows):
+    x, xs, w, ws = dev(*operands(rows, 500, 1040, gen(rows)))
+    a = B.fp8_linear(x, xs, w, ws, torch.float32)
+    for _ in range(3):
+        assert torch.equal(B.fp8_linear(x, xs, w, ws, torch.float32), a)
+    # a row does not depend on the rows beside it within the same kernel form
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    b = B.fp8_grouped(x, xs, off, w[None].contiguous(), ws[None].contiguous(), torch.float32)
+    assert torch.equal(a, b)
+
+
+def test_a_side_stream():
+    x, xs, w, ws = dev(*operands(200, 256, 512, gen(1)))
+    want = B.fp8_linear(x, xs, w, ws)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = B.fp8_linear(x, xs, w, ws)
+    out = torch.zeros_like(want)
+    B.fp8_linear(x, xs, w, ws, out=out, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want) and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("tokens", [2, 40, 500])
+def test_captured_run_replays_as_eager(tokens):
+    """quantize -> grouped -> swiglu -> grouped in one graph, replayed with new
+    inputs and new groups, eager work between."""
+    g = gen(tokens)
+    experts, k, inter = 8, 256, 128
+    x = torch.empty((tokens, k), dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(experts + 1, dtype=torch.int32, device="cuda")
+    w13, s13 = dev(R.random_codes((experts, 2 * inter, k), g), R.random_scales((experts, 2, 2), g))
+    w2, s2 = dev(R.random_codes((experts, k, inter), g), R.random_scales((experts, 2, 1), g))
+
+    def run():
+        c, s = B.fp8_quantize(x)
+        gu = B.fp8_grouped(c, s, off, w13, s13)
+        h, hs = B.fp8_swiglu(gu)
+        return B.fp8_grouped(h, hs, off, w2, s2, torch.float32)
+
+    def fill(seed):
+        q = gen(seed)
+        x.copy_(activations(tokens, k, q, torch.bfloat16))
+        cut = torch.randint(0, tokens + 1, (experts - 1,), generator=q).sort().values.tolist()
+        off.copy_(torch.tensor([0] + cut + [tokens], dtype=torch.int32))
+
+    fill(0)
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for seed in range(1, 6):
+        fill(seed)
+        graph.replay()
+        got = out.clone()
+        assert torch.equal(got, run()), seed
+
+
+def test_refusals():
+    x, xs, w, ws = dev(*operands(4, 128, 256, gen(2)))
+    for bad in (lambda: B.fp8_linear(x, xs[:, :1].contiguous(), w, ws), lambda: B.fp8_linear(x, xs, w[:, :128], ws),
+                lambda: B.fp8_linear(x, xs.cpu(), w, ws), lambda: B.fp8_linear(x.float(), xs, w, ws),
+                lambda: B.fp8_linear(x.t(), xs, w, ws), lambda: B.fp8_linear(x, xs, w, ws, torch.float16),
+                lambda: B.fp8_linear(x, xs, w, ws, out=torch.empty((4, 127), device="cuda")),
+                lambda: B.fp8_quantize(x), lambda: B.fp8_quantize(xs[0]),
+                lambda: B.fp8_swiglu(torch.zeros((2, 33), device="cuda")),
+                lambda: B.fp8_grouped(x, xs, torch.zeros(2, device="cuda"), w[None], ws[None]),
+                lambda: B.fp8_grouped(x, xs, torch.zeros(3, dtype=torch.int32, device="cuda"), w[None], ws[None])):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(B.MoeError) as e:
+        B.fp8_quantize(torch.zeros((2, 24), device="cuda"))
+    assert e.value.status == B.MOE_EUNSUPPORTED
+    with pytest.raises(B.MoeError) as e:
+        B.fp8_quantize(torch.zeros((2, 40), device="cuda")[:, 1:17])
+    assert e.value.status == B.MOE_EALIGN
+
+
+# ---- a run of them together --------------------------------------------------
+
+@pytest.mark.parametrize("tokens", [1, 6, 70, 600])
+def test_layer_in_eight_bits(tokens):
+    """moe_route's routing, then the pooler, the experts and the unpooler in
+    8 bits as a user chains them; each product against 64 bits on the GPU's
+    own inputs, the whole against the layer in 64 bits."""
+    dims = dict(hidden=512, latent=256, inter=128, n_experts=16, top_k=4)
+    H, L, I, E, K = (dims[k] for k in ("hidden", "latent", "inter", "n_experts", "top_k"))
+    g = gen(tokens)
+    x = torch.randn((tokens, H), generator=g).bfloat16().cuda()
+    router = (torch.randn((E, H), generator=g) * 0.05).cuda()
+
+    def weight(*shape):
+        w = torch.randn(shape, generator=g) / shape[-1] ** 0.5
+        b = torch.nn.functional.pad(w, (0, 0, 0, 0)).view(*shape[:-2], shape[-2] // 128, 128, shape[-1] // 128, 128)
+        s = b.abs().amax(dim=(-3, -1)) / 448
+        c = (b / s[..., :, None, :, None]).view(shape).to(F8)
+        return c.cuda(), s.contiguous().cuda()
+
+    pool, w13, w2, unpool = weight(L, H), weight(E, 2 * I, L), weight(E, L, I), weight(H, L)
+    d = B.make_dims(dims)
+    r = B.route(d, x.view(torch.int16), router, B.alloc_workspace(d, tokens))
+    xq = B.fp8_quantize(x)
+    lat = B.fp8_linear(*xq, *pool)
+    lq = B.fp8_quantize(lat)
+    gu = B.fp8_grouped(*lq, r["offsets"], *w13, row_index=r["sorted"], index_div=K)
+    hq = B.fp8_swiglu(gu)
+    rows = B.fp8_grouped(*hq, r["offsets"], *w2, out_dtype=torch.float32)
+    order = r["sorted"].long()
+    normed = rows / (rows.square().mean(1, keepdim=True) + 1e-6).sqrt() * r["w"].reshape(-1)[order][:, None]
+    y = torch.zeros((tokens, L), device="cuda").index_add_(0, order // K, normed).bfloat16()
+    yq = B.fp8_quantize(y)
+    out = B.fp8_linear(*yq, *unpool)
+
+    cpu = lambda ts: [t.cpu() for t in ts]
+    bounds = r["offsets"].tolist()
+    assert bounds[-1] == tokens * K
+    R.assert_product(lat.cpu(), *cpu(xq), *cpu(pool), "pooler")
+    check_grouped(gu.cpu(), *cpu(lq), *cpu(w13), bounds, order.cpu() // K)
+    check_grouped(rows.cpu(), *cpu(hq), *cpu(w2), bounds)
+    R.assert_product(out.cpu(), *cpu(yq), *cpu(unpool), "unpooler")
+    # the layer in 64 bits without any 8-bit activation: four quantisations of
+    # at most 2^-4 per value, their errors independent (rms 2^-4 / sqrt(3) at
+    # the most), through unit-gain random projections; swiglu and the norm at most double it
+    wd = lambda c, s: c.double() * s.double().repeat_interleave(128, -1).repeat_interleave(128, -2)
+    ld = x.double() @ wd(*pool).t()
+    ref = torch.zeros((tokens, L), dtype=torch.float64, device="cuda")
+    for e in range(E):
+        a, b = bounds[e], bounds[e + 1]
+        if a < b:
+            t = order[a:b] // K
+            z = ld[t] @ wd(w13[0][e], w13[1][e]).t()
+            h = torch.nn.functional.silu(z[:, :I]) * z[:, I:]
+            o = h @ wd(w2[0][e], w2[1][e]).t()
+            o = o / (o.square().mean(1, keepdim=True) + 1e-6).sqrt() * r["w"].reshape(-1)[order[a:b]].double()[:, None]
+            ref.index_add_(0, t, o)
+    ref = ref @ wd(*unpool).t()
+    rel = float((out.double() - ref).norm() / ref.norm())
+    assert rel < 4 * 2 * 2.0 ** -4 / 3 ** 0.5, rel
