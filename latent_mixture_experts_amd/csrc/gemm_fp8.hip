@@ -142,106 +142,122 @@ __device__ __forceinline__ void store4(const Fp8Gemm& p, int row, int n, f32x4 v
 }
 
 // ---- few rows: the weights stream once from HBM ----------------------------
-// Workgroup: 16 weight rows x up to 16 * F rows, the blocks of K split over
-// its eight wavefronts (consecutive runs) and joined through LDS in wavefront
-// order. A group of more rows takes them in passes. Grid: (weight row tiles,
-// groups).
+// A wavefront takes 16 weight rows x up to 16 * F rows over a run of K's
+// blocks; KS wavefronts of a workgroup split K and are joined through LDS in
+// order, and the workgroup's 8 / KS such teams take neighbouring weight rows.
+// Everything a block needs (codes of both operands, scales) is loaded to
+// registers D blocks ahead, so each wavefront keeps D * 2 KiB of weights in
+// flight and waits for nothing else. A group of more rows takes them in
+// passes. Grid: (weight row tiles, groups).
 constexpr int kFW = 8;  // wavefronts
-constexpr int kFU = 4;  // blocks loaded together, one such set ahead of the products
 
-template <int F, bool F32>
-__global__ __launch_bounds__(64 * kFW) void fp8_stream_kernel(Fp8Gemm p) {
-  __shared__ f32x4 part[kFW][F][64];
+template <int F, int KS, int D, bool F32>
+__global__ __launch_bounds__(64 * kFW, F <= 2 ? 4 : 2) void fp8_stream_kernel(Fp8Gemm p) {
+  constexpr int kTeams = kFW / KS;
+  __shared__ f32x4 part[KS > 1 ? kFW : 1][F][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nl = lane & 15, g = lane >> 4;
   const Group grp = p.offsets ? find_group(p, static_cast<int>(blockIdx.y), 1 << 30) : Group{0, 0, p.rows};
   if (grp.expert < 0) return;
-  const int n0 = static_cast<int>(blockIdx.x) * 16;
+  const int ks = wave % KS;
+  const int n0 = (static_cast<int>(blockIdx.x) * kTeams + wave / KS) * 16;
   const int nkb = (p.K + kFp8Block - 1) / kFp8Block;
-  const int per = (nkb + kFW - 1) / kFW;
-  const int kb0 = wave * per, kb1 = min(kb0 + per, nkb);
+  const int per = (nkb + KS - 1) / KS;
+  const int kb0 = min(ks * per, nkb), n_kb = min(per, nkb - kb0);
   const size_t K = static_cast<size_t>(p.K);
-  const rsrc_t w_r = make_rsrc(p.w + (static_cast<size_t>(grp.expert) * p.N + n0) * K,
-                               static_cast<uint32_t>(min(16, p.N - n0) * K));
-  const float* ws = p.ws + (static_cast<size_t>(grp.expert) * ((p.N + kFp8Block - 1) / kFp8Block) + n0 / kFp8Block) * nkb;
+  // (a team past the last weight row reads and writes nothing)
+  const int wrows = min(max(p.N - n0, 0), 16);
+  const rsrc_t w_r = make_rsrc(p.w + (static_cast<size_t>(grp.expert) * p.N + n0) * K, static_cast<uint32_t>(wrows * K));
+  const rsrc_t ws_r = make_rsrc(
+      p.ws + (static_cast<size_t>(grp.expert) * ((p.N + kFp8Block - 1) / kFp8Block) + n0 / kFp8Block) * nkb,
+      wrows > 0 ? nkb * 4u : 0u);
   const uint32_t w_off = static_cast<uint32_t>(nl) * p.K + g * 16;
 
   for (int r0 = grp.begin; r0 < grp.end; r0 += 16 * F) {
     const int base = p.index ? 0 : r0;  // the descriptors start at this row of x
-    const int rows_here = p.index ? p.x_rows : grp.end - r0;
+    const int xrows = p.index ? p.x_rows : min(grp.end - r0, 16 * F);
     const rsrc_t x_r = make_rsrc(p.x + static_cast<size_t>(base) * p.ldx,
-                                 static_cast<uint32_t>(static_cast<size_t>(min(rows_here, p.index ? rows_here : 16 * F) - 1) * p.ldx + K));
-    uint32_t x_off[F];
-    const float* xs[F];
-    bool live[F];
+                                 static_cast<uint32_t>(static_cast<size_t>(xrows - 1) * p.ldx + K));
+    const rsrc_t xs_r = make_rsrc(p.xs + static_cast<size_t>(base) * nkb, static_cast<uint32_t>(xrows) * nkb * 4u);
+    uint32_t x_off[F], xs_off[F];  // (lanes without a row read nothing)
 #pragma unroll
     for (int f = 0; f < F; ++f) {
       const int r = r0 + f * 16 + nl;
-      live[f] = r < grp.end;
-      const int src = live[f] ? source_row(p, r) : base;
-      x_off[f] = live[f] ? static_cast<uint32_t>((src - base) * p.ldx) + g * 16 : kOutOfRange;
-      xs[f] = p.xs + static_cast<size_t>(src) * nkb;
+      const int src = r < grp.end ? source_row(p, r) - base : 0;
+      x_off[f] = r < grp.end ? static_cast<uint32_t>(src * p.ldx) + g * 16 : kOutOfRange;
+      xs_off[f] = r < grp.end ? static_cast<uint32_t>(src) * nkb * 4u : kOutOfRange;
     }
     f32x4 acc[F];
 #pragma unroll
     for (int f = 0; f < F; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    uint4 wv[2][kFU][2];
-    // (blocks past this wavefront's run and pieces past the last value read
-    // nothing and give zeros)
-    auto at = [&](uint32_t off, int kb, int half) -> uint32_t {
-      const int k = kb * kFp8Block + half * 64 + g * 16;
-      return kb < kb1 && k < p.K ? off + kb * kFp8Block + half * 64 : kOutOfRange;
-    };
-    auto load_w = [&](int kb, int set) __attribute__((always_inline)) {
+    uint4 wv[D][2], xv[D][F][2];
+    float xsv[D][F], wsv[D];
+    auto load = [&](int u, int i) __attribute__((always_inline)) {
+      const int kb = kb0 + i;
+      const uint32_t at = static_cast<uint32_t>(kb) * kFp8Block;
 #pragma unroll
-      for (int u = 0; u < kFU; ++u)
+      for (int h = 0; h < 2; ++h) {  // (pieces past the last value: zeros in both operands)
+        const bool in = static_cast<int>(at) + h * 64 + g * 16 < p.K;
+        wv[u][h] = buf_load16<kAuxStream>(w_r, in ? w_off + at + h * 64 : kOutOfRange);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) wv[set][u][h] = buf_load16<kAuxStream>(w_r, at(w_off, kb + u, h));
-    };
-    auto step = [&](int kb, int set) __attribute__((always_inline)) {
-      if (kb + kFU < kb1) load_w(kb + kFU, set ^ 1);
-      uint4 xv[F][kFU][2];
-      float sc[F][kFU];
-#pragma unroll
-      for (int u = 0; u < kFU; ++u) {
-        const int kc = min(kb + u, nkb - 1);
-        const float wsc = ws[kc];
-#pragma unroll
-        for (int f = 0; f < F; ++f) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            xv[f][u][h] = buf_load16<kAuxDefault>(x_r, live[f] ? at(x_off[f], kb + u, h) : kOutOfRange);
-          sc[f][u] = xs[f][kc] * wsc;
-        }
+        for (int f = 0; f < F; ++f) xv[u][f][h] = buf_load16<kAuxDefault>(x_r, in ? x_off[f] + at + h * 64 : kOutOfRange);
       }
 #pragma unroll
-      for (int u = 0; u < kFU; ++u) {
-        if (kb + u >= kb1) break;  // (uniform)
+      for (int f = 0; f < F; ++f) xsv[u][f] = __uint_as_float(buf_load4<kAuxDefault>(xs_r, xs_off[f] + kb * 4));
+      wsv[u] = __uint_as_float(buf_load4<kAuxDefault>(ws_r, kb * 4));
+    };
+    auto consume = [&](int u) __attribute__((always_inline)) {
+      const i32x8 wf = pair16(wv[u][0], wv[u][1]);
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-          const f32x4 d = mfma_block<true>(pair16(wv[set][u][0], wv[set][u][1]), pair16(xv[f][u][0], xv[f][u][1]));
+      for (int f = 0; f < F; ++f) {
+        const f32x4 d = mfma_block<true>(wf, pair16(xv[u][f][0], xv[u][f][1]));
+        const float s = xsv[u][f] * wsv[u];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[f][i] = fmaf(d[i], sc[f][u], acc[f][i]);
-        }
+        for (int i = 0; i < 4; ++i) acc[f][i] = fmaf(d[i], s, acc[f][i]);
       }
     };
-    if (kb0 < kb1) load_w(kb0, 0);
-    for (int kb = kb0; kb < kb1; kb += 2 * kFU) {
-      step(kb, 0);
-      if (kb + kFU < kb1) step(kb + kFU, 1);
+#pragma unroll
+    for (int u = 0; u < D; ++u)
+      if (u < n_kb) load(u, u);
+    int i = 0;
+    for (; i + 2 * D <= n_kb; i += D) {  // (no branches inside: the waits stay D blocks deep)
+#pragma unroll
+      for (int u = 0; u < D; ++u) {
+        consume(u);
+        load(u, i + D + u);
+      }
     }
 #pragma unroll
-    for (int f = 0; f < F; ++f) part[wave][f][lane] = acc[f];
-    __syncthreads();
-    if (wave < F) {
-      f32x4 s = part[0][wave][lane];
+    for (int u = 0; u < D; ++u)
+      if (i + u < n_kb) {
+        consume(u);
+        if (i + D + u < n_kb) load(u, i + D + u);
+      }
+    i += D;
 #pragma unroll
-      for (int v = 1; v < kFW; ++v) s += part[v][wave][lane];
-      const int r = r0 + wave * 16 + nl;
-      if (r < grp.end) store4<F32>(p, r, n0 + 4 * g, s);
+    for (int u = 0; u < D; ++u)
+      if (i + u < n_kb) consume(u);
+
+    if constexpr (KS == 1) {
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const int r = r0 + f * 16 + nl;
+        if (r < grp.end && n0 + 4 * g < p.N) store4<F32>(p, r, n0 + 4 * g, acc[f]);
+      }
+    } else {
+#pragma unroll
+      for (int f = 0; f < F; ++f) part[wave][f][lane] = acc[f];
+      __syncthreads();
+      for (int f = ks; f < F; f += KS) {
+        f32x4 s = part[wave - ks][f][lane];
+#pragma unroll
+        for (int v = 1; v < KS; ++v) s += part[wave - ks + v][f][lane];
+        const int r = r0 + f * 16 + nl;
+        if (r < grp.end && n0 + 4 * g < p.N) store4<F32>(p, r, n0 + 4 * g, s);
+      }
+      __syncthreads();  // (the next pass writes part again)
     }
-    __syncthreads();  // (the next pass writes part again)
   }
 }
 
@@ -435,15 +451,26 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
   }
 }
 
-template <int F>
+template <int F, int KS, int D>
+hipError_t launch_stream_ks(const Fp8Gemm& g, int tiles, int groups, hipStream_t st) {
+  const dim3 grid((tiles * KS + kFW - 1) / kFW, groups), block(64 * kFW);
+  if (g.f32)
+    MOE_LAUNCH((fp8_stream_kernel<F, KS, D, true>), grid, block, 0, st, g);
+  else
+    MOE_LAUNCH((fp8_stream_kernel<F, KS, D, false>), grid, block, 0, st, g);
+  return hipGetLastError();
+}
+
+template <int F, int D>
 hipError_t launch_stream(const Fp8Gemm& g, hipStream_t st) {
   const int groups = g.offsets ? std::min(g.rows, g.experts) : 1;
-  const dim3 grid((g.N + 15) / 16, groups), block(64 * kFW);
-  if (g.f32)
-    MOE_LAUNCH((fp8_stream_kernel<F, true>), grid, block, 0, st, g);
-  else
-    MOE_LAUNCH((fp8_stream_kernel<F, false>), grid, block, 0, st, g);
-  return hipGetLastError();
+  const int tiles = (g.N + 15) / 16;
+  // K split over wavefronts until about 16 of them per CU have work
+  const int64_t waves = static_cast<int64_t>(tiles) * groups;
+  if (waves >= 4096) return launch_stream_ks<F, 1, D>(g, tiles, groups, st);
+  if (waves >= 2048) return launch_stream_ks<F, 2, D>(g, tiles, groups, st);
+  if (waves >= 1024) return launch_stream_ks<F, 4, D>(g, tiles, groups, st);
+  return launch_stream_ks<F, 8, D>(g, tiles, groups, st);
 }
 
 template <int WT, int WW, int FT, int FW>
@@ -469,9 +496,10 @@ hipError_t launch_tile(const Fp8Gemm& g, hipStream_t st) {
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t st) {
   // rows that see one weight row, on average over the experts
   const int64_t avg = g.offsets ? (static_cast<int64_t>(g.rows) + g.experts - 1) / g.experts : g.rows;
-  if (avg <= 16) return launch_stream<1>(g, st);
-  if (avg <= 32) return launch_stream<2>(g, st);
-  if (avg <= 64) return launch_stream<4>(g, st);
+  if (avg <= 16) return launch_stream<1, 4>(g, st);
+  if (avg <= 32) return launch_stream<2, 2>(g, st);
+  if (avg <= 48) return launch_stream<3, 4>(g, st);
+  if (avg <= 64) return launch_stream<4, 3>(g, st);
   return launch_tile<2, 4, 4, 4>(g, st);
 }
 
