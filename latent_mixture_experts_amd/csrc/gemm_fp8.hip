@@ -25,6 +25,15 @@ namespace moe {
 
 namespace {
 
+// Waits until at most the N most recent vector-memory instructions are
+// outstanding (N < 64: vmcnt's high two bits are bits 14 and 15) and every LDS
+// read has returned.
+template <int N>
+__device__ __forceinline__ void wait_vm_lds() {
+  static_assert(N >= 0 && N < 64, "vmcnt field");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
+}
+
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // Eight E4M3 codes as bf16, exactly.
@@ -41,14 +50,28 @@ __device__ __forceinline__ bf16x8 e4m3x8_to_bf16(int lo, int hi) {
 // l%16 of A and column l%16 of B; the 32 bytes of lane group l/16 may be any
 // 32 of the block's 128 as long as both operands take the same ones, since
 // the block is summed whole. It receives D rows 4*(l/16) .. +3 of column l%16.
-// EXACT: through bf16.
+// An operand fragment as the matrix instructions take it: the codes, or
+// (EXACT) their bf16 values, decoded once for all the products it enters.
 template <bool EXACT>
-__device__ __forceinline__ f32x4 mfma_block(i32x8 a, i32x8 b) {
-  f32x4 d{0.f, 0.f, 0.f, 0.f};
-  if constexpr (!EXACT) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, d, 0, 0, 0, 0, 0, 0);
+struct Operand {
+  i32x8 codes;
+  __device__ __forceinline__ void set(i32x8 c) { codes = c; }
+};
+template <>
+struct Operand<true> {
+  bf16x8 v[4];
+  __device__ __forceinline__ void set(i32x8 c) {
 #pragma unroll
-  for (int s = 0; s < 4; ++s)
-    d = mfma16x16x32(e4m3x8_to_bf16(a[2 * s], a[2 * s + 1]), e4m3x8_to_bf16(b[2 * s], b[2 * s + 1]), d);
+    for (int s = 0; s < 4; ++s) v[s] = e4m3x8_to_bf16(c[2 * s], c[2 * s + 1]);
+  }
+};
+__device__ __forceinline__ f32x4 mfma_block(const Operand<false>& a, const Operand<false>& b) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.codes, b.codes, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma_block(const Operand<true>& a, const Operand<true>& b) {
+  f32x4 d{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < 4; ++s) d = mfma16x16x32(a.v[s], b.v[s], d);
   return d;
 }
 
@@ -208,10 +231,12 @@ __global__ __launch_bounds__(64 * kFW, F <= 2 ? 4 : 2) void fp8_stream_kernel(Fp
       wsv[u] = __uint_as_float(buf_load4<kAuxDefault>(ws_r, kb * 4));
     };
     auto consume = [&](int u) __attribute__((always_inline)) {
-      const i32x8 wf = pair16(wv[u][0], wv[u][1]);
+      Operand<true> wf, xf;
+      wf.set(pair16(wv[u][0], wv[u][1]));
 #pragma unroll
       for (int f = 0; f < F; ++f) {
-        const f32x4 d = mfma_block<true>(wf, pair16(xv[u][f][0], xv[u][f][1]));
+        xf.set(pair16(xv[u][f][0], xv[u][f][1]));
+        const f32x4 d = mfma_block(wf, xf);
         const float s = xsv[u][f] * wsv[u];
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[f][i] = fmaf(d[i], s, acc[f][i]);
@@ -263,29 +288,41 @@ __global__ __launch_bounds__(64 * kFW, F <= 2 ? 4 : 2) void fp8_stream_kernel(Fp
 
 // ---- many rows: LDS-staged tiles -------------------------------------------
 // Workgroup tile: WT x WW wavefronts, each FT x FW fragments of 16 rows x 16
-// weight rows. One block of K per stage: both operands' 128-byte rows are
-// copied straight from global memory into LDS (two stages, the copies of the
-// next under the products of this one), 16-byte piece c of row r at position
-// r*8 + (c ^ ((r/2) % 8)), so that the 16 rows one read touches start in
-// distinct banks. The scales follow in LDS in sets of four stages, loaded to
-// registers one set ahead.
+// weight rows; a tile's row fragments are dealt to the wavefront rows in
+// turn, so a partly filled tile loads them evenly. One block of K per stage:
+// both operands' 128-byte rows are copied straight from global memory into
+// LDS in a ring of R stages (the copies run R - 1 ahead), 16-byte piece c of
+// row r at position r*8 + (c ^ ((r/2) % 8)), so that the 16 rows one read
+// touches start in distinct banks. The scales follow the same way in sets of
+// four stages, [row][stage], two sets in turn.
 constexpr int kFSet = 4;
 
 __device__ __forceinline__ int fpos(int r, int c) { return (r * 8 + (c ^ ((r >> 1) & 7))) * 16; }
 
-template <int WT, int WW, int FT, int FW, bool F32>
+// As lds_copy16, 4 bytes per lane.
+__device__ __forceinline__ void lds_copy4(rsrc_t r, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(r), "s"(lds) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ uint32_t lds_address(const T* p) {
+  return static_cast<uint32_t>(reinterpret_cast<size_t>((__attribute__((address_space(3))) T*)(p)));
+}
+
+template <int WT, int WW, int FT, int FW, int R, bool F32>
 __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n_row_tiles, int n_col_tiles) {
   constexpr int NW = WT * WW, BM = WT * FT * 16, BN = WW * FW * 16;
   constexpr int kXOps = BM / 8 / NW, kWOps = BN / 8 / NW;  // 1-KiB copies per wavefront and stage
   constexpr int kThreads = 64 * NW;
-  constexpr int kNB = BN / kFp8Block;                       // weight blocks across the tile
-  constexpr int kSets = kFSet * (BM + kNB);                 // scales of one set
-  constexpr int kPer = (kSets + kThreads - 1) / kThreads;
+  constexpr int kNB = BN / kFp8Block;                     // weight blocks across the tile
+  constexpr int kSOps = BM / 16 / NW;                     // 64-scale copies per wavefront and set: 16 rows each
   static_assert(BN % kFp8Block == 0 && kXOps * 8 * NW == BM && kWOps * 8 * NW == BN, "whole copies");
-  __shared__ __attribute__((aligned(1024))) uint8_t Xs[2][BM * kFp8Block];
-  __shared__ __attribute__((aligned(1024))) uint8_t Ws[2][BN * kFp8Block];
-  __shared__ float Sc[2][kSets];  // [set parity][stage in set][row, then weight block]
-  __shared__ int src[BM];         // source row of each tile row
+  static_assert(kSOps * 16 * NW == BM && kNB * kFSet <= 64 && NW >= 2, "whole scale copies");
+  constexpr int kOps = kXOps + kWOps;
+  static_assert((R - 2) * kOps < 64, "vmcnt field");
+  __shared__ __attribute__((aligned(1024))) uint8_t Xs[R][BM * kFp8Block];
+  __shared__ __attribute__((aligned(1024))) uint8_t Ws[R][BN * kFp8Block];
+  __shared__ __attribute__((aligned(256))) float Sx[2][BM * kFSet];
+  __shared__ __attribute__((aligned(256))) float Sw[2][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nl = lane & 15, g = lane >> 4;
   const int wt = wave % WT, ww = wave / WT;
@@ -307,74 +344,80 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
   const int nrows = grp.end - grp.begin, n0 = nt * BN, ncols = min(BN, p.N - n0);
   const int nkb = (p.K + kFp8Block - 1) / kFp8Block;
   const size_t K = static_cast<size_t>(p.K);
-  const rsrc_t w_r = make_rsrc(p.w + (static_cast<size_t>(grp.expert) * p.N + n0) * K, static_cast<uint32_t>(ncols * K));
-  const float* ws = p.ws + (static_cast<size_t>(grp.expert) * ((p.N + kFp8Block - 1) / kFp8Block) + n0 / kFp8Block) * nkb;
+  const int nnb = (ncols + kFp8Block - 1) / kFp8Block;  // weight blocks of the tile that exist
+  const uint8_t* w_base = p.w + (static_cast<size_t>(grp.expert) * p.N + n0) * K;
+  const uint32_t w_bytes = static_cast<uint32_t>(ncols * K);
+  const rsrc_t ws_r = make_rsrc(
+      p.ws + (static_cast<size_t>(grp.expert) * ((p.N + kFp8Block - 1) / kFp8Block) + n0 / kFp8Block) * nkb,
+      static_cast<uint32_t>(nnb * nkb) * 4u);
   const int base = p.index ? 0 : grp.begin;
-  const rsrc_t x_r = make_rsrc(p.x + static_cast<size_t>(base) * p.ldx,
-                               static_cast<uint32_t>(static_cast<size_t>((p.index ? p.x_rows : nrows) - 1) * p.ldx + K));
-  for (int r = tid; r < BM; r += kThreads) src[r] = r < nrows ? source_row(p, grp.begin + r) : -1;
-  __syncthreads();
+  const int xrows = p.index ? p.x_rows : nrows;
+  const uint8_t* x_base = p.x + static_cast<size_t>(base) * p.ldx;
+  const uint32_t x_bytes = static_cast<uint32_t>(static_cast<size_t>(xrows - 1) * p.ldx + K);
+  const rsrc_t xs_r = make_rsrc(p.xs + static_cast<size_t>(base) * nkb, static_cast<uint32_t>(xrows) * nkb * 4u);
+  auto row_of = [&](int r) -> int { return r < nrows ? source_row(p, grp.begin + r) - base : -1; };
 
-  // source offsets of this wavefront's copies, and this lane's value offset in a block
-  uint32_t xoff[kXOps], woff[kWOps];
-  int xk[kXOps], wk[kWOps];
+  // Source offsets of this wavefront's copies in the first stage; the
+  // descriptors step along K, so a copy costs no vector arithmetic.
+  uint32_t xoff[kXOps], woff[kWOps], soff[kSOps];
 #pragma unroll
   for (int i = 0; i < kXOps; ++i) {
-    const int r = (kXOps * wave + i) * 8 + (lane >> 3);
-    xk[i] = ((lane & 7) ^ ((r >> 1) & 7)) * 16;
-    xoff[i] = src[r] < 0 ? kOutOfRange : static_cast<uint32_t>((src[r] - base) * p.ldx) + xk[i];
+    const int r = (kXOps * wave + i) * 8 + (lane >> 3), src = row_of(r);
+    xoff[i] = src < 0 ? kOutOfRange : static_cast<uint32_t>(src * p.ldx) + ((lane & 7) ^ ((r >> 1) & 7)) * 16;
   }
 #pragma unroll
   for (int i = 0; i < kWOps; ++i) {
     const int r = (kWOps * wave + i) * 8 + (lane >> 3);
-    wk[i] = ((lane & 7) ^ ((r >> 1) & 7)) * 16;
-    woff[i] = static_cast<uint32_t>(r) * p.K + wk[i];
+    woff[i] = static_cast<uint32_t>(r) * p.K + ((lane & 7) ^ ((r >> 1) & 7)) * 16;
   }
-  const uint32_t lds_x = static_cast<uint32_t>(reinterpret_cast<size_t>(
-      (__attribute__((address_space(3))) uint8_t*)(&Xs[0][0])));
-  const uint32_t lds_w = static_cast<uint32_t>(reinterpret_cast<size_t>(
-      (__attribute__((address_space(3))) uint8_t*)(&Ws[0][0])));
-  auto issue = [&](int st, int slot) __attribute__((always_inline)) {
-    const int k0 = st * kFp8Block;
-    // (pieces past the last value read nothing: zeros in both operands)
 #pragma unroll
-    for (int i = 0; i < kXOps; ++i)
-      lds_copy16(x_r, xk[i] + k0 < p.K ? xoff[i] + k0 : kOutOfRange,
-                 __builtin_amdgcn_readfirstlane(lds_x + slot * (BM * kFp8Block) + (kXOps * wave + i) * 1024));
-#pragma unroll
-    for (int i = 0; i < kWOps; ++i)
-      lds_copy16(w_r, wk[i] + k0 < p.K ? woff[i] + k0 : kOutOfRange,
-                 __builtin_amdgcn_readfirstlane(lds_w + slot * (BN * kFp8Block) + (kWOps * wave + i) * 1024));
+  for (int i = 0; i < kSOps; ++i) {
+    const int src = row_of((kSOps * wave + i) * 16 + (lane >> 2));
+    soff[i] = src < 0 ? kOutOfRange : static_cast<uint32_t>(src) * nkb * 4u + (lane & 3) * 4;
+  }
+  const uint32_t lds_x = lds_address(&Xs[0][0]), lds_w = lds_address(&Ws[0][0]);
+  const uint32_t lds_sx = lds_address(&Sx[0][0]), lds_sw = lds_address(&Sw[0][0]);
+  // Copies of one stage: descriptors, and the LDS slot they fill. Stages past
+  // the last have empty descriptors, so their copies read nothing (zeros into a
+  // slot that no product reads) and every stage counts the same.
+  struct Stage {
+    rsrc_t x, w;
+    int slot;
   };
-
-  // scales of one set: this thread's kPer of them
-  const float* sp[kPer];
-  int sq[kPer];
+  const bool partial = p.K % kFp8Block != 0;
+  auto stage_of = [&](int st, int slot) __attribute__((always_inline)) {
+    const uint32_t k0 = static_cast<uint32_t>(st) * kFp8Block;
+    if (partial && st == nkb - 1) {  // the last one that reads: its pieces past K read nothing, zeros in both operands
+      auto in = [&](int q) { return static_cast<int>(k0) + ((lane & 7) ^ (((q * 8 + (lane >> 3)) >> 1) & 7)) * 16 < p.K; };
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = tid + j * kThreads, c = i / kFSet;  // four consecutive threads: one row's four stages
-    sq[j] = i % kFSet;
-    if (i >= kSets)
-      sp[j] = nullptr;
-    else if (c < BM)
-      sp[j] = src[c] < 0 ? nullptr : p.xs + static_cast<size_t>(src[c]) * nkb;
+      for (int i = 0; i < kXOps; ++i)
+        if (!in(kXOps * wave + i)) xoff[i] = kOutOfRange;
+#pragma unroll
+      for (int i = 0; i < kWOps; ++i)
+        if (!in(kWOps * wave + i)) woff[i] = kOutOfRange;
+    }
+    const bool none = st >= nkb;
+    return Stage{make_rsrc(none ? x_base : x_base + k0, none ? 0 : x_bytes - k0),
+                 make_rsrc(none ? w_base : w_base + k0, none ? 0 : w_bytes - k0), slot};
+  };
+  // this wavefront's copy c (0 .. kOps-1) of a stage
+  auto copy = [&](const Stage& s, int c) __attribute__((always_inline)) {
+    if (c < kXOps)
+      lds_copy16(s.x, xoff[c < kXOps ? c : 0],
+                 __builtin_amdgcn_readfirstlane(lds_x + s.slot * (BM * kFp8Block) + (kXOps * wave + c) * 1024));
     else
-      sp[j] = (c - BM) * kFp8Block < ncols ? ws + static_cast<size_t>(c - BM) * nkb : nullptr;
-  }
-  float sv[kPer];
-  auto load_set = [&](int set) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int kb = set * kFSet + sq[j];
-      sv[j] = sp[j] && kb < nkb ? sp[j][kb] : 0.0f;
-    }
+      lds_copy16(s.w, woff[c < kXOps ? 0 : c - kXOps],
+                 __builtin_amdgcn_readfirstlane(lds_w + s.slot * (BN * kFp8Block) + (kWOps * wave + c - kXOps) * 1024));
   };
-  auto store_set = [&](int set) __attribute__((always_inline)) {
+  auto issue_set = [&](int set) __attribute__((always_inline)) {
+    const bool in = set * kFSet + (lane & 3) < nkb;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int i = tid + j * kThreads;
-      if (i < kSets) Sc[set & 1][sq[j] * (BM + kNB) + i / kFSet] = sv[j];
-    }
+    for (int i = 0; i < kSOps; ++i)
+      lds_copy4(xs_r, in ? soff[i] + set * (kFSet * 4) : kOutOfRange,
+                __builtin_amdgcn_readfirstlane(lds_sx + (set & 1) * (BM * kFSet * 4) + (kSOps * wave + i) * 256));
+    if (wave == 0)
+      lds_copy4(ws_r, in && (lane >> 2) < nnb ? ((lane >> 2) * nkb + set * kFSet + (lane & 3)) * 4u : kOutOfRange,
+                __builtin_amdgcn_readfirstlane(lds_sw + (set & 1) * 256));
   };
 
   f32x4 acc[FT][FW];
@@ -383,55 +426,126 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
 #pragma unroll
     for (int f = 0; f < FW; ++f) acc[t][f] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  auto compute = [&](int st, int slot, auto live_tag) __attribute__((always_inline)) {
-    constexpr int LIVE = decltype(live_tag)::value;
-    if constexpr (LIVE > 0) {
-      const float* sc = &Sc[(st / kFSet) & 1][(st % kFSet) * (BM + kNB)];
-      const float wsc = sc[BM + ww * (FW * 16) / kFp8Block];
-      i32x8 wv[FW];
-#pragma unroll
-      for (int f = 0; f < FW; ++f) {
-        const int r = (ww * FW + f) * 16 + nl;
-        wv[f] = pair16(*reinterpret_cast<const uint4*>(&Ws[slot][fpos(r, g)]),
-                       *reinterpret_cast<const uint4*>(&Ws[slot][fpos(r, 4 + g)]));
-      }
-#pragma unroll
-      for (int t = 0; t < LIVE; ++t) {
-        const int r = (wt * FT + t) * 16 + nl;
-        const i32x8 xv = pair16(*reinterpret_cast<const uint4*>(&Xs[slot][fpos(r, g)]),
-                                *reinterpret_cast<const uint4*>(&Xs[slot][fpos(r, 4 + g)]));
-        const float s = sc[r] * wsc;
-#pragma unroll
-        for (int f = 0; f < FW; ++f) {
-          const f32x4 d = mfma_block<F32>(wv[f], xv);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[t][f][i] = fmaf(d[i], s, acc[t][f][i]);
-        }
-      }
-    }
-  };
-
+  // Stage st lives in slot st % R. The stages overlap: before the last row
+  // fragment's products of a stage every wavefront has read its slot to
+  // registers; there they meet, the first fragments of stage st + 1 (landed by
+  // then) are read under those last products, and the slot takes the copies of
+  // stage st + R, spread over the following products (together they would fill
+  // the memory pipe's queue and hold the wavefront up). Within a stage a
+  // product's four scaled additions run under the matrix instructions of the two
+  // products after it, and the next row fragment's reads under those of this
+  // one; the scheduling barriers keep that order (left alone, the compiler puts
+  // all additions behind all products).
   auto kloop = [&](auto live_tag) __attribute__((always_inline)) {
-    load_set(0);
-    issue(0, 0);
-    store_set(0);
-    wait_vm_keep<0>();
-    __syncthreads();
-    for (int st = 0; st < nkb; ++st) {
-      const int slot = st & 1;
-      if (st + 1 < nkb) issue(st + 1, slot ^ 1);
-      const bool first = st % kFSet == 0, last = st % kFSet == kFSet - 1;
-      if (first) load_set(st / kFSet + 1);
-      compute(st, slot, live_tag);
-      if (last) store_set(st / kFSet + 1);
-      wait_vm_keep<0>();  // stage st + 1 has landed
-      __syncthreads();
+    constexpr int LIVE = decltype(live_tag)::value;
+    constexpr int kProducts = LIVE * FW;  // of a wavefront and stage
+    // copy c goes out with product at(c), counted from the meeting
+    auto at = [](int c) constexpr { return kProducts >= 2 * kOps ? 2 * c : c * kProducts / kOps; };
+    auto copies_at = [&](const Stage& s, int q) __attribute__((always_inline)) {
+#pragma unroll
+      for (int c = 0; c < kOps; ++c)
+        if (at(c) == q) copy(s, c);
+    };
+    issue_set(0);
+#pragma unroll
+    for (int s = 0; s < R - 1; ++s) {
+      const Stage g = stage_of(s, s);
+#pragma unroll
+      for (int c = 0; c < kOps; ++c) copy(g, c);
     }
+    Stage ahead = stage_of(R - 1, R - 1);
+#pragma unroll
+    for (int q = 0; q < (LIVE > 0 ? FW : 1); ++q) copies_at(ahead, q);
+    wait_vm_lds<0>();
+    __syncthreads();
+    // the copies of stage st + 1 have landed, in every wavefront
+    auto meet = [&](int st, int slot) __attribute__((always_inline)) {
+      wait_vm_lds<(R - 2) * kOps>();
+      __syncthreads();
+      ahead = stage_of(st + R, slot);
+    };
+    if constexpr (LIVE == 0) {
+      for (int st = 0, slot = 0; st < nkb; ++st, slot = slot == R - 1 ? 0 : slot + 1) {
+        if (st % kFSet == 0) issue_set(st / kFSet + 1);
+        meet(st, slot);
+        copies_at(ahead, 0);
+      }
+    } else {
+      // (rows 16 apart keep their swizzle: constant offsets from one address)
+      const int xp0 = fpos(wt * 16 + nl, g), xp1 = fpos(wt * 16 + nl, 4 + g);
+      const int wp0 = fpos(ww * FW * 16 + nl, g), wp1 = fpos(ww * FW * 16 + nl, 4 + g);
+      auto read_x = [&](int slot, int t) __attribute__((always_inline)) {
+        const uint8_t* b = &Xs[0][0] + slot * (BM * kFp8Block);
+        return pair16(*reinterpret_cast<const uint4*>(b + xp0 + t * WT * 2048), *reinterpret_cast<const uint4*>(b + xp1 + t * WT * 2048));
+      };
+      auto read_w = [&](int slot, int f) __attribute__((always_inline)) {
+        const uint8_t* b = &Ws[0][0] + slot * (BN * kFp8Block);
+        return pair16(*reinterpret_cast<const uint4*>(b + wp0 + f * 2048), *reinterpret_cast<const uint4*>(b + wp1 + f * 2048));
+      };
+      auto scale_x = [&](int st, int t) __attribute__((always_inline)) {
+        return (&Sx[(st / kFSet) & 1][(wt * 16 + nl) * kFSet + st % kFSet])[t * WT * 16 * kFSet];
+      };
+      auto scale_w = [&](int st) __attribute__((always_inline)) {
+        return Sw[(st / kFSet) & 1][ww * (FW * 16) / kFp8Block * kFSet + st % kFSet];
+      };
+      Operand<F32> wv[FW], xv;
+#pragma unroll
+      for (int f = 0; f < FW; ++f) wv[f].set(read_w(0, f));
+      i32x8 next = read_x(0, 0);
+      float next_s = scale_x(0, 0), next_w = scale_w(0);
+      constexpr int kLag = 2;
+      for (int st = 0, slot = 0; st < nkb; ++st) {
+        const int after = slot == R - 1 ? 0 : slot + 1;
+        const float wsc = next_w;
+        // (every wavefront has read the last scales of the set this one replaces)
+        if (st % kFSet == 0) issue_set(st / kFSet + 1);
+        f32x4 d[kLag + 1];
+        float s[2];
+        auto add = [&](int j) __attribute__((always_inline)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            acc[j / FW][j % FW][i] = fmaf(d[j % (kLag + 1)][i], s[(j / FW) & 1], acc[j / FW][j % FW][i]);
+            asm volatile("" : "+v"(acc[j / FW][j % FW][i]));  // (not moved behind the branches below)
+          }
+        };
+#pragma unroll
+        for (int t = 0; t < LIVE; ++t) {
+          xv.set(next);
+          s[t & 1] = next_s * wsc;
+          if (t + 1 < LIVE) {
+            next = read_x(slot, t + 1);
+            next_s = scale_x(st, t + 1);
+          } else {
+            meet(st, slot);
+            next = read_x(after, 0);  // (after the last stage: what the slot held, not used)
+            next_s = scale_x(st + 1, 0);
+            next_w = scale_w(st + 1);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int f = 0; f < FW; ++f) {
+            const int j = t * FW + f;
+            d[j % (kLag + 1)] = mfma_block(wv[f], xv);
+            __builtin_amdgcn_sched_barrier(0);
+            if (t + 1 == LIVE) wv[f].set(read_w(after, f));
+            if (j >= kLag) add(j - kLag);
+            copies_at(ahead, t + 1 == LIVE ? f : j + FW);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+#pragma unroll
+        for (int j = LIVE * FW - kLag; j < LIVE * FW; ++j) add(j);
+        slot = after;
+      }
+    }
+    wait_vm_lds<0>();  // (a last scale set and empty copies may still be on their way into this workgroup's LDS)
   };
-  // fragments of this wavefront that hold rows, rounded up to a compiled count
-  const int live = (min(max(nrows - wt * FT * 16, 0), FT * 16) + 15) / 16;
-  if (live > FT / 2)
+  // fragments of this wavefront that hold rows
+  const int live = ((nrows + 15) / 16 + WT - 1 - wt) / WT;
+  if (live > FT * 3 / 4)
     kloop(std::integral_constant<int, FT>{});
+  else if (live > FT / 2)
+    kloop(std::integral_constant<int, FT * 3 / 4>{});
   else if (live > FT / 4)
     kloop(std::integral_constant<int, FT / 2>{});
   else if (live > 0)
@@ -441,7 +555,7 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
 
 #pragma unroll
   for (int t = 0; t < FT; ++t) {
-    const int r = (wt * FT + t) * 16 + nl;
+    const int r = (t * WT + wt) * 16 + nl;
     if (r >= nrows) continue;
 #pragma unroll
     for (int f = 0; f < FW; ++f) {
@@ -473,7 +587,7 @@ hipError_t launch_stream(const Fp8Gemm& g, hipStream_t st) {
   return launch_stream_ks<F, 8, D>(g, tiles, groups, st);
 }
 
-template <int WT, int WW, int FT, int FW>
+template <int WT, int WW, int FT, int FW, int R>
 hipError_t launch_tile(const Fp8Gemm& g, hipStream_t st) {
   constexpr int BM = WT * FT * 16, BN = WW * FW * 16;
   const int nct = (g.N + BN - 1) / BN;
@@ -485,9 +599,9 @@ hipError_t launch_tile(const Fp8Gemm& g, hipStream_t st) {
     grid = (nrt * nct + 7) / 8 * 8;
   }
   if (g.f32)
-    MOE_LAUNCH((fp8_tile_kernel<WT, WW, FT, FW, true>), dim3(grid), dim3(64 * WT * WW), 0, st, g, nrt, nct);
+    MOE_LAUNCH((fp8_tile_kernel<WT, WW, FT, FW, R, true>), dim3(grid), dim3(64 * WT * WW), 0, st, g, nrt, nct);
   else
-    MOE_LAUNCH((fp8_tile_kernel<WT, WW, FT, FW, false>), dim3(grid), dim3(64 * WT * WW), 0, st, g, nrt, nct);
+    MOE_LAUNCH((fp8_tile_kernel<WT, WW, FT, FW, R, false>), dim3(grid), dim3(64 * WT * WW), 0, st, g, nrt, nct);
   return hipGetLastError();
 }
 
@@ -500,7 +614,10 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t st) {
   if (avg <= 32) return launch_stream<2, 2>(g, st);
   if (avg <= 48) return launch_stream<3, 4>(g, st);
   if (avg <= 64) return launch_stream<4, 3>(g, st);
-  return launch_tile<2, 4, 4, 4>(g, st);
+#ifndef FP8_TILE
+#define FP8_TILE 2, 4, 4, 4, 3
+#endif
+  return launch_tile<FP8_TILE>(g, st);
 }
 
 }  // namespace moe
