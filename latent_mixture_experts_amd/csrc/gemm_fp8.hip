@@ -17,6 +17,9 @@
 // rounded to bf16 (2^-9 each), not for fp32 ones. There, and wherever the
 // weights' way from HBM bounds the kernel anyway, the codes become bf16 (exact)
 // and four bf16 MFMAs 16x16x32 sum the block to fp32 (measured: 1e-8 of the norm).
+#include <algorithm>
+#include <cmath>
+
 #include "device_common.h"
 #include "fp8.h"
 #include "kernels.h"
@@ -195,6 +198,11 @@ __global__ __launch_bounds__(64 * kFW, F <= 2 ? 4 : 2) void fp8_stream_kernel(Fp
       p.ws + (static_cast<size_t>(grp.expert) * ((p.N + kFp8Block - 1) / kFp8Block) + n0 / kFp8Block) * nkb,
       wrows > 0 ? nkb * 4u : 0u);
   const uint32_t w_off = static_cast<uint32_t>(nl) * p.K + g * 16;
+  // Wavefronts that take all of K start at different blocks: weight rows lie a
+  // power of two apart as a rule, and wavefronts that walk them in step meet on
+  // the same memory channels (32 verified tokens' down projection 557 -> 510 us).
+  const int turn =
+      KS == 1 ? __builtin_amdgcn_readfirstlane((5 * (static_cast<int>(blockIdx.x) + wave) + static_cast<int>(blockIdx.y)) % nkb) : 0;
 
   for (int r0 = grp.begin; r0 < grp.end; r0 += 16 * F) {
     const int base = p.index ? 0 : r0;  // the descriptors start at this row of x
@@ -217,7 +225,8 @@ __global__ __launch_bounds__(64 * kFW, F <= 2 ? 4 : 2) void fp8_stream_kernel(Fp
     uint4 wv[D][2], xv[D][F][2];
     float xsv[D][F], wsv[D];
     auto load = [&](int u, int i) __attribute__((always_inline)) {
-      const int kb = kb0 + i;
+      const int turned = i + turn;
+      const int kb = kb0 + (turned >= n_kb ? turned - n_kb : turned);
       const uint32_t at = static_cast<uint32_t>(kb) * kFp8Block;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // (pieces past the last value: zeros in both operands)
@@ -312,13 +321,14 @@ template <int WT, int WW, int FT, int FW, int R, bool F32>
 __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n_row_tiles, int n_col_tiles) {
   constexpr int NW = WT * WW, BM = WT * FT * 16, BN = WW * FW * 16;
   constexpr int kXOps = BM / 8 / NW, kWOps = BN / 8 / NW;  // 1-KiB copies per wavefront and stage
-  constexpr int kThreads = 64 * NW;
-  constexpr int kNB = BN / kFp8Block;                     // weight blocks across the tile
-  constexpr int kSOps = BM / 16 / NW;                     // 64-scale copies per wavefront and set: 16 rows each
-  static_assert(BN % kFp8Block == 0 && kXOps * 8 * NW == BM && kWOps * 8 * NW == BN, "whole copies");
-  static_assert(kSOps * 16 * NW == BM && kNB * kFSet <= 64 && NW >= 2, "whole scale copies");
+  constexpr int kSOps = (BM / 16 + NW - 1) / NW;           // 64-scale copies per wavefront and set: 16 rows each
+  static_assert((BN % kFp8Block == 0 || kFp8Block % BN == 0) && BN * kFSet <= 64 * kFp8Block, "tiles within weight blocks");
+  static_assert(kXOps * 8 * NW == BM && kWOps * 8 * NW == BN && BM % 16 == 0, "whole copies");
   constexpr int kOps = kXOps + kWOps;
   static_assert((R - 2) * kOps < 64, "vmcnt field");
+  // (a set is asked for four stages before its first use, and the wait of the
+  // third of them leaves the copies of R - 2 stages outstanding, all younger)
+  static_assert(R >= 2 && R <= 4, "scale sets land in time");
   __shared__ __attribute__((aligned(1024))) uint8_t Xs[R][BM * kFp8Block];
   __shared__ __attribute__((aligned(1024))) uint8_t Ws[R][BN * kFp8Block];
   __shared__ __attribute__((aligned(256))) float Sx[2][BM * kFSet];
@@ -344,7 +354,7 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
   const int nrows = grp.end - grp.begin, n0 = nt * BN, ncols = min(BN, p.N - n0);
   const int nkb = (p.K + kFp8Block - 1) / kFp8Block;
   const size_t K = static_cast<size_t>(p.K);
-  const int nnb = (ncols + kFp8Block - 1) / kFp8Block;  // weight blocks of the tile that exist
+  const int nnb = (n0 % kFp8Block + ncols + kFp8Block - 1) / kFp8Block;  // weight blocks of the tile that exist
   const uint8_t* w_base = p.w + (static_cast<size_t>(grp.expert) * p.N + n0) * K;
   const uint32_t w_bytes = static_cast<uint32_t>(ncols * K);
   const rsrc_t ws_r = make_rsrc(
@@ -413,8 +423,9 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
     const bool in = set * kFSet + (lane & 3) < nkb;
 #pragma unroll
     for (int i = 0; i < kSOps; ++i)
-      lds_copy4(xs_r, in ? soff[i] + set * (kFSet * 4) : kOutOfRange,
-                __builtin_amdgcn_readfirstlane(lds_sx + (set & 1) * (BM * kFSet * 4) + (kSOps * wave + i) * 256));
+      if (kSOps * wave + i < BM / 16)
+        lds_copy4(xs_r, in ? soff[i] + set * (kFSet * 4) : kOutOfRange,
+                  __builtin_amdgcn_readfirstlane(lds_sx + (set & 1) * (BM * kFSet * 4) + (kSOps * wave + i) * 256));
     if (wave == 0)
       lds_copy4(ws_r, in && (lane >> 2) < nnb ? ((lane >> 2) * nkb + set * kFSet + (lane & 3)) * 4u : kOutOfRange,
                 __builtin_amdgcn_readfirstlane(lds_sw + (set & 1) * 256));
@@ -486,14 +497,14 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
         return (&Sx[(st / kFSet) & 1][(wt * 16 + nl) * kFSet + st % kFSet])[t * WT * 16 * kFSet];
       };
       auto scale_w = [&](int st) __attribute__((always_inline)) {
-        return Sw[(st / kFSet) & 1][ww * (FW * 16) / kFp8Block * kFSet + st % kFSet];
+        return Sw[(st / kFSet) & 1][(n0 % kFp8Block + ww * (FW * 16)) / kFp8Block * kFSet + st % kFSet];
       };
       Operand<F32> wv[FW], xv;
 #pragma unroll
       for (int f = 0; f < FW; ++f) wv[f].set(read_w(0, f));
       i32x8 next = read_x(0, 0);
       float next_s = scale_x(0, 0), next_w = scale_w(0);
-      constexpr int kLag = 2;
+      constexpr int kLag = FW < 2 ? FW : 2;  // (two row fragments' scales are held)
       for (int st = 0, slot = 0; st < nkb; ++st) {
         const int after = slot == R - 1 ? 0 : slot + 1;
         const float wsc = next_w;
@@ -534,7 +545,7 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
           }
         }
 #pragma unroll
-        for (int j = LIVE * FW - kLag; j < LIVE * FW; ++j) add(j);
+        for (int j = kProducts > kLag ? kProducts - kLag : 0; j < kProducts; ++j) add(j);
         slot = after;
       }
     }
@@ -545,11 +556,11 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
   if (live > FT * 3 / 4)
     kloop(std::integral_constant<int, FT>{});
   else if (live > FT / 2)
-    kloop(std::integral_constant<int, FT * 3 / 4>{});
+    kloop(std::integral_constant<int, (FT > 2 ? FT * 3 / 4 : FT)>{});
   else if (live > FT / 4)
-    kloop(std::integral_constant<int, FT / 2>{});
+    kloop(std::integral_constant<int, (FT > 1 ? FT / 2 : 1)>{});
   else if (live > 0)
-    kloop(std::integral_constant<int, (FT / 4 > 0 ? FT / 4 : 1)>{});
+    kloop(std::integral_constant<int, (FT > 4 ? FT / 4 : 1)>{});
   else
     kloop(std::integral_constant<int, 0>{});
 
@@ -575,20 +586,22 @@ hipError_t launch_stream_ks(const Fp8Gemm& g, int tiles, int groups, hipStream_t
   return hipGetLastError();
 }
 
+// K is split over wavefronts until about 16 of them per CU have work (one
+// token's gate/up, 8 experts x 512 tiles: no split 57 us, split by two 59);
+// a wavefront with all of K keeps four blocks in flight, one with a part two
+// (one pooler token 9.3 -> 8.8 us, fewer registers).
 template <int F, int D>
-hipError_t launch_stream(const Fp8Gemm& g, hipStream_t st) {
-  const int groups = g.offsets ? std::min(g.rows, g.experts) : 1;
+hipError_t launch_stream(const Fp8Gemm& g, int groups, hipStream_t st) {
   const int tiles = (g.N + 15) / 16;
-  // K split over wavefronts until about 16 of them per CU have work
   const int64_t waves = static_cast<int64_t>(tiles) * groups;
   if (waves >= 4096) return launch_stream_ks<F, 1, D>(g, tiles, groups, st);
-  if (waves >= 2048) return launch_stream_ks<F, 2, D>(g, tiles, groups, st);
-  if (waves >= 1024) return launch_stream_ks<F, 4, D>(g, tiles, groups, st);
-  return launch_stream_ks<F, 8, D>(g, tiles, groups, st);
+  if (waves >= 2048) return launch_stream_ks<F, 2, 2>(g, tiles, groups, st);
+  if (waves >= 1024) return launch_stream_ks<F, 4, 2>(g, tiles, groups, st);
+  return launch_stream_ks<F, 8, 2>(g, tiles, groups, st);
 }
 
-template <int WT, int WW, int FT, int FW, int R>
-hipError_t launch_tile(const Fp8Gemm& g, hipStream_t st) {
+template <int WT, int WW, int FT, int FW, int R, bool F32>
+hipError_t launch_tile_as(const Fp8Gemm& g, hipStream_t st) {
   constexpr int BM = WT * FT * 16, BN = WW * FW * 16;
   const int nct = (g.N + BN - 1) / BN;
   int nrt = (g.rows + BM - 1) / BM, grid;
@@ -598,26 +611,74 @@ hipError_t launch_tile(const Fp8Gemm& g, hipStream_t st) {
   } else {
     grid = (nrt * nct + 7) / 8 * 8;
   }
-  if (g.f32)
-    MOE_LAUNCH((fp8_tile_kernel<WT, WW, FT, FW, R, true>), dim3(grid), dim3(64 * WT * WW), 0, st, g, nrt, nct);
-  else
-    MOE_LAUNCH((fp8_tile_kernel<WT, WW, FT, FW, R, false>), dim3(grid), dim3(64 * WT * WW), 0, st, g, nrt, nct);
+  MOE_LAUNCH((fp8_tile_kernel<WT, WW, FT, FW, R, F32>), dim3(grid), dim3(64 * WT * WW), 0, st, g, nrt, nct);
   return hipGetLastError();
+}
+template <int WT, int WW, int FT, int FW, int R>
+hipError_t launch_tile(const Fp8Gemm& g, hipStream_t st) {
+  return g.f32 ? launch_tile_as<WT, WW, FT, FW, R, true>(g, st) : launch_tile_as<WT, WW, FT, FW, R, false>(g, st);
+}
+
+// The tiles, smallest first: rows, weight rows, and what a stage (one block of
+// K) takes in ns: in the first round of workgroups, and in each further one
+// (the small ones share a CU with others, so their further rounds overlap).
+// Measured at K = 8192 in bf16 out; fp32 out takes about 1.7 times as long in all.
+// The small tiles win while they fit one round, since each then has a CU to
+// itself and its stages wait on memory, not on the matrix unit; e.g. N = 4096,
+// K = 8192, us (32x64 / 64x64 / 64x128 / 128x128 / 128x256 / 256x256):
+//   128 rows  23 / 25 / 28 / 36 / 53 / 72      512 rows  51 / 34 / 31 / 37 / 54 / 87
+//   2048 rows 205 / 131 / 119 / 82 / 71 / 99   4096 rows - / - / - / - / 155 / 126
+struct TileShape {
+  int rows, cols, first_ns, more_ns;
+};
+constexpr TileShape kTiles[] = {{32, 64, 340, 210},   {64, 64, 390, 260},   {64, 128, 450, 450},
+                                {128, 128, 620, 620}, {128, 256, 1100, 1100}, {256, 256, 1800, 1800}};
+
+int best_tile(const Fp8Gemm& g) {
+  // rows of one group: experts get theirs unevenly, by about the root of the mean
+  const double mean = static_cast<double>(g.rows) / g.experts;
+  const double rows = g.experts > 1 ? mean + std::sqrt(mean) : mean;
+  const int groups = std::min(g.rows, g.experts);
+  int best = 0;
+  double least = 0.0;
+  for (int i = 0; i < 6; ++i) {
+    const TileShape& t = kTiles[i];
+    // 256 x 256: its sums fill the registers, no room for bf16 operands; and
+    // partly filled ones waste most (experts of 128 rows: 1153 us against 1051)
+    if (t.rows == 256 && (g.f32 || (g.experts > 1 && mean < 512))) continue;
+    const double tiles = groups * std::ceil(rows / t.rows) * std::ceil(static_cast<double>(g.N) / t.cols);
+    const double rounds = t.more_ns == t.first_ns ? std::ceil(tiles / 256.0) : std::max(1.0, tiles / 256.0);
+    const double ns = t.first_ns + (rounds - 1.0) * t.more_ns;
+    if (i == 0 || ns < least) {
+      least = ns;
+      best = i;
+    }
+  }
+  return best;
 }
 
 }  // namespace
 
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t st) {
-  // rows that see one weight row, on average over the experts
-  const int64_t avg = g.offsets ? (static_cast<int64_t>(g.rows) + g.experts - 1) / g.experts : g.rows;
-  if (avg <= 16) return launch_stream<1, 4>(g, st);
-  if (avg <= 32) return launch_stream<2, 2>(g, st);
-  if (avg <= 48) return launch_stream<3, 4>(g, st);
-  if (avg <= 64) return launch_stream<4, 3>(g, st);
-#ifndef FP8_TILE
-#define FP8_TILE 2, 4, 4, 4, 3
-#endif
-  return launch_tile<FP8_TILE>(g, st);
+  const int groups = std::min(g.rows, g.experts);
+  const int mean = (g.rows - 1) / g.experts + 1;
+  // Few rows and little to stream: the streaming kernel (one pooler token 9 us
+  // against 18 with 32 x 64 tiles, one token's gate/up 57 against 72). Where
+  // the tiles fill the chip several times over they read faster, whole
+  // 128-byte lines at a time (32 tokens' down projection 481 us against 510).
+  if (g.rows <= 64 && mean <= 16 && static_cast<int64_t>(groups) * ((g.N + 63) / 64) < 2048)
+    return launch_stream<1, 4>(g, groups, st);
+  // (17 .. 32 rows, deep and narrow: N = 4096, K = 8192 17 us against 21; N =
+  // 8192, K = 4096 18 against 13)
+  if (g.experts == 1 && g.rows <= 32 && g.N <= g.K) return launch_stream<2, 2>(g, groups, st);
+  switch (best_tile(g)) {
+    case 0: return launch_tile<1, 4, 2, 1, 4>(g, st);
+    case 1: return launch_tile<2, 2, 2, 2, 4>(g, st);
+    case 2: return launch_tile<2, 4, 2, 2, 4>(g, st);
+    case 3: return launch_tile<2, 4, 4, 2, 4>(g, st);
+    case 4: return launch_tile<2, 4, 4, 4, 3>(g, st);
+    default: return launch_tile_as<2, 4, 8, 4, 2, false>(g, st);
+  }
 }
 
 }  // namespace moe

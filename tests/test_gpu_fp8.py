@@ -160,6 +160,35 @@ def test_linear(rows, n, k, dtype):
     R.assert_product(got.cpu(), x, xs, w, ws)
 
 
+# (rows, n, k) that fill the chip with each tile size, with ragged rows, weight rows and blocks of K
+WIDE = [(30, 9000, 400), (70, 8200, 1040), (200, 4100, 400), (300, 5000, 272), (500, 4200, 1168), (520, 8200, 144),
+        (1030, 8200, 144), (2100, 4200, 528), (2300, 8200, 256), (511, 20001, 144)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,n,k", WIDE)
+def test_linear_wide(rows, n, k, dtype):
+    ops = dev(*operands(rows, n, k, gen(rows * 3 + n + k)))
+    R.assert_product(B.fp8_linear(*ops, dtype), *ops)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("experts,mean,n,k", [(90, 1, 2100, 272), (256, 20, 300, 144), (30, 40, 2100, 400),
+                                              (60, 40, 3000, 144), (30, 60, 4200, 144), (30, 130, 2100, 272),
+                                              (4, 600, 4200, 144), (3, 1700, 2100, 528), (8, 375, 700, 1040)])
+def test_grouped_wide(experts, mean, n, k, dtype):
+    """Uneven groups, some empty, for each tile size."""
+    g = gen(experts + mean + n)
+    part = torch.rand(experts, generator=g)
+    part[part < 0.15] = 0.0
+    part[0] += 1.0
+    sizes = (part / part.sum() * mean * experts).round().int().tolist()
+    bounds = [0] + torch.tensor(sizes).cumsum(0).tolist()
+    x, xs, w, ws = dev(*operands(bounds[-1], n, k, g, experts))
+    got = B.fp8_grouped(x, xs, torch.tensor(bounds, dtype=torch.int32).cuda(), w, ws, dtype)
+    check_grouped(got, x, xs, w, ws, bounds)
+
+
 @pytest.mark.parametrize("rows", [1, 20, 40, 150])
 def test_every_position_counts_once(rows):
     """One nonzero code per row of x and every code value in w: out is that code times the scales."""
@@ -223,7 +252,7 @@ def sizes_case(name, experts, g):
 def check_grouped(got, x, xs, w, ws, bounds, rows_of=None):
     for e, (a, b) in enumerate(zip(bounds, bounds[1:])):
         if b > a:
-            at = torch.arange(a, b) if rows_of is None else rows_of[a:b]
+            at = torch.arange(a, b, device=x.device) if rows_of is None else rows_of[a:b]
             R.assert_product(got[a:b], x[at], xs[at], w[e], ws[e], e)
 
 
