@@ -311,11 +311,13 @@ def _pitch(t: torch.Tensor) -> int:
 
 def _run(what: str, dev: torch.device, stream, *args) -> None:
     fn = getattr(lib(), what)
+    # (the current stream's handle alone: building a torch.cuda.Stream costs as much as the launch)
+    st = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
     if dev.index == torch.cuda.current_device():
-        rc = fn(*args, _stream(stream))
+        rc = fn(*args, st)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, _stream(stream))
+            rc = fn(*args, st)
     if rc != MOE_OK:
         raise MoeError(rc, what)
 

@@ -14,8 +14,7 @@ struct Balance {
   // forward
   int32_t* counts;       // [E + 1]: routes per expert, tokens that count
   float* loss;           // [2]: balance, z
-  float* part;           // workspace, [workgroups][E + 1]: probability sums, lse^2 sum
-  int32_t* part_counts;  // workspace, [workgroups][E + 1]
+  void* part;            // workspace: partial sums of every workgroup
   // backward
   const int32_t* counts_in;
   const float* dloss;     // [2]
@@ -23,7 +22,7 @@ struct Balance {
   const float* dw;        // [T][K] their gradients; both or neither
   float* dlogits;         // [T][E]
 };
-int balance_workgroups(int T);
+size_t balance_workspace(int T, int E);  // bytes; 0: none needed
 hipError_t launch_balance_loss(const Balance& b, hipStream_t st);
 hipError_t launch_balance_backward(const Balance& b, hipStream_t st);
 

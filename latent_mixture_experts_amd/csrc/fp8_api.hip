@@ -183,8 +183,7 @@ int moe_fp8_grouped(int32_t rows, int32_t n_experts, int32_t N, int32_t K, const
 
 size_t moe_balance_workspace_bytes(int32_t T, int32_t n_experts) {
   if (check_balance(T, n_experts, 1) != MOE_OK) return 0;
-  const int G = moe::balance_workgroups(T);
-  return G == 1 ? 0 : static_cast<size_t>(G) * (n_experts + 1) * 8;
+  return moe::balance_workspace(T, n_experts);
 }
 
 int moe_balance_loss_validate(int32_t T, int32_t n_experts, int32_t top_k, const float* logits,
@@ -220,9 +219,7 @@ int moe_balance_loss(int32_t T, int32_t n_experts, int32_t top_k, const float* l
   b.K = top_k;
   b.counts = counts;
   b.loss = losses;
-  const size_t half = static_cast<size_t>(moe::balance_workgroups(T)) * (n_experts + 1);
-  b.part = static_cast<float*>(workspace);
-  b.part_counts = workspace ? reinterpret_cast<int32_t*>(b.part + half) : nullptr;
+  b.part = workspace;
   return moe::report_hip(moe::launch_balance_loss(b, static_cast<hipStream_t>(hip_stream)));
 }
 
