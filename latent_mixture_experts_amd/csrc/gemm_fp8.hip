@@ -298,13 +298,16 @@ __global__ __launch_bounds__(64 * kFW, F <= 2 ? 4 : 2) void fp8_stream_kernel(Fp
 // ---- many rows: LDS-staged tiles -------------------------------------------
 // Workgroup tile: WT x WW wavefronts, each FT x FW fragments of 16 rows x 16
 // weight rows; a tile's row fragments are dealt to the wavefront rows in
-// turn, so a partly filled tile loads them evenly. One block of K per stage:
-// both operands' 128-byte rows are copied straight from global memory into
-// LDS in a ring of R stages (the copies run R - 1 ahead), 16-byte piece c of
-// row r at position r*8 + (c ^ ((r/2) % 8)), so that the 16 rows one read
-// touches start in distinct banks. The scales follow the same way in sets of
-// four stages, [row][stage], two sets in turn.
-constexpr int kFSet = 4;
+// turn, so a partly filled tile loads them evenly. KG blocks of K per stage,
+// each the work of a wavefront group of its own (WT x WW), joined through LDS at
+// the end: with few tiles a stage's length is the time its parts wait for each
+// other, and a stage of four blocks takes little longer than one of one. Both
+// operands' 128-byte rows are copied straight from global memory into LDS in a
+// ring of R stages (the copies run R - 1 ahead), 16-byte piece c of row r at
+// position r*8 + (c ^ ((r/2) % 8)), so that the 16 rows one read touches start
+// in distinct banks. The scales follow the same way: with one block per stage
+// in sets of four stages, [row][stage], two sets in turn; else with their stage,
+// [row][block].
 
 __device__ __forceinline__ int fpos(int r, int c) { return (r * 8 + (c ^ ((r >> 1) & 7))) * 16; }
 
@@ -317,25 +320,28 @@ __device__ __forceinline__ uint32_t lds_address(const T* p) {
   return static_cast<uint32_t>(reinterpret_cast<size_t>((__attribute__((address_space(3))) T*)(p)));
 }
 
-template <int WT, int WW, int FT, int FW, int R, bool F32>
-__global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n_row_tiles, int n_col_tiles) {
-  constexpr int NW = WT * WW, BM = WT * FT * 16, BN = WW * FW * 16;
-  constexpr int kXOps = BM / 8 / NW, kWOps = BN / 8 / NW;  // 1-KiB copies per wavefront and stage
-  constexpr int kSOps = (BM / 16 + NW - 1) / NW;           // 64-scale copies per wavefront and set: 16 rows each
+template <int WT, int WW, int FT, int FW, int R, int KG, bool F32>
+__global__ __launch_bounds__(64 * WT * WW * KG) void fp8_tile_kernel(Fp8Gemm p, int n_row_tiles, int n_col_tiles) {
+  constexpr int kGroup = WT * WW, NW = kGroup * KG, BM = WT * FT * 16, BN = WW * FW * 16;
+  constexpr int kXOps = BM / 8 / kGroup, kWOps = BN / 8 / kGroup;  // 1-KiB copies per wavefront and stage (its group's block)
+  constexpr int kFSet = KG == 1 ? 4 : KG;                          // blocks of a scale set
+  constexpr int kSetRows = 64 / kFSet, kSets = KG == 1 ? 2 : R;    // rows of one 64-scale copy; sets held
+  constexpr int kSOps = (BM / kSetRows + NW - 1) / NW;             // such copies per wavefront and set
   static_assert((BN % kFp8Block == 0 || kFp8Block % BN == 0) && BN * kFSet <= 64 * kFp8Block, "tiles within weight blocks");
-  static_assert(kXOps * 8 * NW == BM && kWOps * 8 * NW == BN && BM % 16 == 0, "whole copies");
+  static_assert(kXOps * 8 * kGroup == BM && kWOps * 8 * kGroup == BN && BM % kSetRows == 0, "whole copies");
   constexpr int kOps = kXOps + kWOps;
   static_assert((R - 2) * kOps < 64, "vmcnt field");
-  // (a set is asked for four stages before its first use, and the wait of the
-  // third of them leaves the copies of R - 2 stages outstanding, all younger)
+  // (KG = 1: a set is asked for four stages before its first use, and the wait
+  // of the third of them leaves the copies of R - 2 stages outstanding, all younger)
   static_assert(R >= 2 && R <= 4, "scale sets land in time");
-  __shared__ __attribute__((aligned(1024))) uint8_t Xs[R][BM * kFp8Block];
-  __shared__ __attribute__((aligned(1024))) uint8_t Ws[R][BN * kFp8Block];
-  __shared__ __attribute__((aligned(256))) float Sx[2][BM * kFSet];
-  __shared__ __attribute__((aligned(256))) float Sw[2][64];
+  constexpr int kXSlot = KG * BM * kFp8Block, kWSlot = KG * BN * kFp8Block;  // bytes of a stage
+  __shared__ __attribute__((aligned(1024))) uint8_t Xs[R][kXSlot];
+  __shared__ __attribute__((aligned(1024))) uint8_t Ws[R][kWSlot];
+  __shared__ __attribute__((aligned(256))) float Sx[kSets][BM * kFSet];
+  __shared__ __attribute__((aligned(256))) float Sw[kSets][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nl = lane & 15, g = lane >> 4;
-  const int wt = wave % WT, ww = wave / WT;
+  const int kg = wave / kGroup, wt = wave % kGroup % WT, ww = wave % kGroup / WT;
 
   int mt, nt;
   if (p.offsets) {  // an expert's row tiles share its weights in one XCD's L2
@@ -352,7 +358,7 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
   const Group grp = find_group(p, mt, BM);
   if (grp.expert < 0) return;
   const int nrows = grp.end - grp.begin, n0 = nt * BN, ncols = min(BN, p.N - n0);
-  const int nkb = (p.K + kFp8Block - 1) / kFp8Block;
+  const int nkb = (p.K + kFp8Block - 1) / kFp8Block, nst = (nkb + KG - 1) / KG;
   const size_t K = static_cast<size_t>(p.K);
   const int nnb = (n0 % kFp8Block + ncols + kFp8Block - 1) / kFp8Block;  // weight blocks of the tile that exist
   const uint8_t* w_base = p.w + (static_cast<size_t>(grp.expert) * p.N + n0) * K;
@@ -372,18 +378,18 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
   uint32_t xoff[kXOps], woff[kWOps], soff[kSOps];
 #pragma unroll
   for (int i = 0; i < kXOps; ++i) {
-    const int r = (kXOps * wave + i) * 8 + (lane >> 3), src = row_of(r);
-    xoff[i] = src < 0 ? kOutOfRange : static_cast<uint32_t>(src * p.ldx) + ((lane & 7) ^ ((r >> 1) & 7)) * 16;
+    const int r = (kXOps * (wave % kGroup) + i) * 8 + (lane >> 3), src = row_of(r);
+    xoff[i] = src < 0 ? kOutOfRange : static_cast<uint32_t>(src * p.ldx) + kg * kFp8Block + ((lane & 7) ^ ((r >> 1) & 7)) * 16;
   }
 #pragma unroll
   for (int i = 0; i < kWOps; ++i) {
-    const int r = (kWOps * wave + i) * 8 + (lane >> 3);
-    woff[i] = static_cast<uint32_t>(r) * p.K + ((lane & 7) ^ ((r >> 1) & 7)) * 16;
+    const int r = (kWOps * (wave % kGroup) + i) * 8 + (lane >> 3);
+    woff[i] = static_cast<uint32_t>(r) * p.K + kg * kFp8Block + ((lane & 7) ^ ((r >> 1) & 7)) * 16;
   }
 #pragma unroll
   for (int i = 0; i < kSOps; ++i) {
-    const int src = row_of((kSOps * wave + i) * 16 + (lane >> 2));
-    soff[i] = src < 0 ? kOutOfRange : static_cast<uint32_t>(src) * nkb * 4u + (lane & 3) * 4;
+    const int src = row_of((kSOps * wave + i) * kSetRows + lane / kFSet);
+    soff[i] = src < 0 ? kOutOfRange : static_cast<uint32_t>(src) * nkb * 4u + (lane % kFSet) * 4;
   }
   const uint32_t lds_x = lds_address(&Xs[0][0]), lds_w = lds_address(&Ws[0][0]);
   const uint32_t lds_sx = lds_address(&Sx[0][0]), lds_sw = lds_address(&Sw[0][0]);
@@ -394,19 +400,20 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
     rsrc_t x, w;
     int slot;
   };
-  const bool partial = p.K % kFp8Block != 0;
+  const bool partial = p.K % (KG * kFp8Block) != 0;
   auto stage_of = [&](int st, int slot) __attribute__((always_inline)) {
-    const uint32_t k0 = static_cast<uint32_t>(st) * kFp8Block;
-    if (partial && st == nkb - 1) {  // the last one that reads: its pieces past K read nothing, zeros in both operands
-      auto in = [&](int q) { return static_cast<int>(k0) + ((lane & 7) ^ (((q * 8 + (lane >> 3)) >> 1) & 7)) * 16 < p.K; };
+    const uint32_t k0 = static_cast<uint32_t>(st) * (KG * kFp8Block);
+    if (partial && st == nst - 1) {  // the last one that reads: its pieces past K read nothing, zeros in both operands
+      const int left = p.K - static_cast<int>(k0) - kg * kFp8Block;
+      auto in = [&](int q) { return ((lane & 7) ^ (((q * 8 + (lane >> 3)) >> 1) & 7)) * 16 < left; };
 #pragma unroll
       for (int i = 0; i < kXOps; ++i)
-        if (!in(kXOps * wave + i)) xoff[i] = kOutOfRange;
+        if (!in(kXOps * (wave % kGroup) + i)) xoff[i] = kOutOfRange;
 #pragma unroll
       for (int i = 0; i < kWOps; ++i)
-        if (!in(kWOps * wave + i)) woff[i] = kOutOfRange;
+        if (!in(kWOps * (wave % kGroup) + i)) woff[i] = kOutOfRange;
     }
-    const bool none = st >= nkb;
+    const bool none = st >= nst;
     return Stage{make_rsrc(none ? x_base : x_base + k0, none ? 0 : x_bytes - k0),
                  make_rsrc(none ? w_base : w_base + k0, none ? 0 : w_bytes - k0), slot};
   };
@@ -414,21 +421,21 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
   auto copy = [&](const Stage& s, int c) __attribute__((always_inline)) {
     if (c < kXOps)
       lds_copy16(s.x, xoff[c < kXOps ? c : 0],
-                 __builtin_amdgcn_readfirstlane(lds_x + s.slot * (BM * kFp8Block) + (kXOps * wave + c) * 1024));
+                 __builtin_amdgcn_readfirstlane(lds_x + s.slot * kXSlot + (kXOps * wave + c) * 1024));
     else
       lds_copy16(s.w, woff[c < kXOps ? 0 : c - kXOps],
-                 __builtin_amdgcn_readfirstlane(lds_w + s.slot * (BN * kFp8Block) + (kWOps * wave + c - kXOps) * 1024));
+                 __builtin_amdgcn_readfirstlane(lds_w + s.slot * kWSlot + (kWOps * wave + c - kXOps) * 1024));
   };
-  auto issue_set = [&](int set) __attribute__((always_inline)) {
-    const bool in = set * kFSet + (lane & 3) < nkb;
+  auto issue_set = [&](int set, int at) __attribute__((always_inline)) {
+    const bool in = set * kFSet + lane % kFSet < nkb;
 #pragma unroll
     for (int i = 0; i < kSOps; ++i)
-      if (kSOps * wave + i < BM / 16)
+      if (kSOps * wave + i < BM / kSetRows)
         lds_copy4(xs_r, in ? soff[i] + set * (kFSet * 4) : kOutOfRange,
-                  __builtin_amdgcn_readfirstlane(lds_sx + (set & 1) * (BM * kFSet * 4) + (kSOps * wave + i) * 256));
+                  __builtin_amdgcn_readfirstlane(lds_sx + at * (BM * kFSet * 4) + (kSOps * wave + i) * 256));
     if (wave == 0)
-      lds_copy4(ws_r, in && (lane >> 2) < nnb ? ((lane >> 2) * nkb + set * kFSet + (lane & 3)) * 4u : kOutOfRange,
-                __builtin_amdgcn_readfirstlane(lds_sw + (set & 1) * 256));
+      lds_copy4(ws_r, in && lane / kFSet < nnb ? (lane / kFSet * nkb + set * kFSet + lane % kFSet) * 4u : kOutOfRange,
+                __builtin_amdgcn_readfirstlane(lds_sw + at * 256));
   };
 
   f32x4 acc[FT][FW];
@@ -457,13 +464,15 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
       for (int c = 0; c < kOps; ++c)
         if (at(c) == q) copy(s, c);
     };
-    issue_set(0);
+    if constexpr (KG == 1) issue_set(0, 0);
 #pragma unroll
     for (int s = 0; s < R - 1; ++s) {
+      if constexpr (KG > 1) issue_set(s, s);
       const Stage g = stage_of(s, s);
 #pragma unroll
       for (int c = 0; c < kOps; ++c) copy(g, c);
     }
+    if constexpr (KG > 1) issue_set(R - 1, R - 1);
     Stage ahead = stage_of(R - 1, R - 1);
 #pragma unroll
     for (int q = 0; q < (LIVE > 0 ? FW : 1); ++q) copies_at(ahead, q);
@@ -473,11 +482,17 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
     auto meet = [&](int st, int slot) __attribute__((always_inline)) {
       wait_vm_lds<(R - 2) * kOps>();
       __syncthreads();
+      if constexpr (KG > 1) issue_set(st + R, slot);
       ahead = stage_of(st + R, slot);
     };
+    // KG = 1: the set after stage st's, when st is the first of its set (every
+    // wavefront has read the last scales of the set this one replaces)
+    auto next_set = [&](int st) __attribute__((always_inline)) {
+      if (KG == 1 && st % kFSet == 0) issue_set(st / kFSet + 1, (st / kFSet + 1) & 1);
+    };
     if constexpr (LIVE == 0) {
-      for (int st = 0, slot = 0; st < nkb; ++st, slot = slot == R - 1 ? 0 : slot + 1) {
-        if (st % kFSet == 0) issue_set(st / kFSet + 1);
+      for (int st = 0, slot = 0; st < nst; ++st, slot = slot == R - 1 ? 0 : slot + 1) {
+        next_set(st);
         meet(st, slot);
         copies_at(ahead, 0);
       }
@@ -486,30 +501,31 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
       const int xp0 = fpos(wt * 16 + nl, g), xp1 = fpos(wt * 16 + nl, 4 + g);
       const int wp0 = fpos(ww * FW * 16 + nl, g), wp1 = fpos(ww * FW * 16 + nl, 4 + g);
       auto read_x = [&](int slot, int t) __attribute__((always_inline)) {
-        const uint8_t* b = &Xs[0][0] + slot * (BM * kFp8Block);
+        const uint8_t* b = &Xs[0][0] + slot * kXSlot + kg * (BM * kFp8Block);
         return pair16(*reinterpret_cast<const uint4*>(b + xp0 + t * WT * 2048), *reinterpret_cast<const uint4*>(b + xp1 + t * WT * 2048));
       };
       auto read_w = [&](int slot, int f) __attribute__((always_inline)) {
-        const uint8_t* b = &Ws[0][0] + slot * (BN * kFp8Block);
+        const uint8_t* b = &Ws[0][0] + slot * kWSlot + kg * (BN * kFp8Block);
         return pair16(*reinterpret_cast<const uint4*>(b + wp0 + f * 2048), *reinterpret_cast<const uint4*>(b + wp1 + f * 2048));
       };
-      auto scale_x = [&](int st, int t) __attribute__((always_inline)) {
-        return (&Sx[(st / kFSet) & 1][(wt * 16 + nl) * kFSet + st % kFSet])[t * WT * 16 * kFSet];
+      auto scale_x = [&](int st, int slot, int t) __attribute__((always_inline)) {
+        const int set = KG == 1 ? (st / kFSet) & 1 : slot, blk = KG == 1 ? st % kFSet : kg;
+        return (&Sx[set][(wt * 16 + nl) * kFSet + blk])[t * WT * 16 * kFSet];
       };
-      auto scale_w = [&](int st) __attribute__((always_inline)) {
-        return Sw[(st / kFSet) & 1][(n0 % kFp8Block + ww * (FW * 16)) / kFp8Block * kFSet + st % kFSet];
+      auto scale_w = [&](int st, int slot) __attribute__((always_inline)) {
+        const int set = KG == 1 ? (st / kFSet) & 1 : slot, blk = KG == 1 ? st % kFSet : kg;
+        return Sw[set][(n0 % kFp8Block + ww * (FW * 16)) / kFp8Block * kFSet + blk];
       };
       Operand<F32> wv[FW], xv;
 #pragma unroll
       for (int f = 0; f < FW; ++f) wv[f].set(read_w(0, f));
       i32x8 next = read_x(0, 0);
-      float next_s = scale_x(0, 0), next_w = scale_w(0);
+      float next_s = scale_x(0, 0, 0), next_w = scale_w(0, 0);
       constexpr int kLag = FW < 2 ? FW : 2;  // (two row fragments' scales are held)
-      for (int st = 0, slot = 0; st < nkb; ++st) {
+      for (int st = 0, slot = 0; st < nst; ++st) {
         const int after = slot == R - 1 ? 0 : slot + 1;
         const float wsc = next_w;
-        // (every wavefront has read the last scales of the set this one replaces)
-        if (st % kFSet == 0) issue_set(st / kFSet + 1);
+        next_set(st);
         f32x4 d[kLag + 1];
         float s[2];
         auto add = [&](int j) __attribute__((always_inline)) {
@@ -525,12 +541,12 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
           s[t & 1] = next_s * wsc;
           if (t + 1 < LIVE) {
             next = read_x(slot, t + 1);
-            next_s = scale_x(st, t + 1);
+            next_s = scale_x(st, slot, t + 1);
           } else {
             meet(st, slot);
             next = read_x(after, 0);  // (after the last stage: what the slot held, not used)
-            next_s = scale_x(st + 1, 0);
-            next_w = scale_w(st + 1);
+            next_s = scale_x(st + 1, after, 0);
+            next_w = scale_w(st + 1, after);
           }
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -564,6 +580,25 @@ __global__ __launch_bounds__(64 * WT * WW) void fp8_tile_kernel(Fp8Gemm p, int n
   else
     kloop(std::integral_constant<int, 0>{});
 
+  if constexpr (KG > 1) {  // the groups' sums in order, through the LDS that held the stages
+    static_assert((KG - 1) * kGroup * FT * FW * 1024 <= R * kWSlot, "sums fit");
+    f32x4* part = reinterpret_cast<f32x4*>(&Ws[0][0]);
+    __syncthreads();  // (every wavefront's copies have landed and its reads are done)
+    if (kg > 0) {
+#pragma unroll
+      for (int t = 0; t < FT; ++t)
+#pragma unroll
+        for (int f = 0; f < FW; ++f) part[((wave - kGroup) * FT * FW + t * FW + f) * 64 + lane] = acc[t][f];
+    }
+    __syncthreads();
+    if (kg > 0) return;
+#pragma unroll
+    for (int v = 1; v < KG; ++v)
+#pragma unroll
+      for (int t = 0; t < FT; ++t)
+#pragma unroll
+        for (int f = 0; f < FW; ++f) acc[t][f] += part[((wave + (v - 1) * kGroup) * FT * FW + t * FW + f) * 64 + lane];
+  }
 #pragma unroll
   for (int t = 0; t < FT; ++t) {
     const int r = (t * WT + wt) * 16 + nl;
@@ -600,7 +635,7 @@ hipError_t launch_stream(const Fp8Gemm& g, int groups, hipStream_t st) {
   return launch_stream_ks<F, 8, 2>(g, tiles, groups, st);
 }
 
-template <int WT, int WW, int FT, int FW, int R, bool F32>
+template <int WT, int WW, int FT, int FW, int R, int KG, bool F32>
 hipError_t launch_tile_as(const Fp8Gemm& g, hipStream_t st) {
   constexpr int BM = WT * FT * 16, BN = WW * FW * 16;
   const int nct = (g.N + BN - 1) / BN;
@@ -611,45 +646,53 @@ hipError_t launch_tile_as(const Fp8Gemm& g, hipStream_t st) {
   } else {
     grid = (nrt * nct + 7) / 8 * 8;
   }
-  MOE_LAUNCH((fp8_tile_kernel<WT, WW, FT, FW, R, F32>), dim3(grid), dim3(64 * WT * WW), 0, st, g, nrt, nct);
+  MOE_LAUNCH((fp8_tile_kernel<WT, WW, FT, FW, R, KG, F32>), dim3(grid), dim3(64 * WT * WW * KG), 0, st, g, nrt, nct);
   return hipGetLastError();
 }
-template <int WT, int WW, int FT, int FW, int R>
+template <int WT, int WW, int FT, int FW, int R, int KG>
 hipError_t launch_tile(const Fp8Gemm& g, hipStream_t st) {
-  return g.f32 ? launch_tile_as<WT, WW, FT, FW, R, true>(g, st) : launch_tile_as<WT, WW, FT, FW, R, false>(g, st);
+  return g.f32 ? launch_tile_as<WT, WW, FT, FW, R, KG, true>(g, st) : launch_tile_as<WT, WW, FT, FW, R, KG, false>(g, st);
 }
 
-// The tiles, smallest first: rows, weight rows, and what a stage (one block of
-// K) takes in ns: in the first round of workgroups, and in each further one
-// (the small ones share a CU with others, so their further rounds overlap).
-// Measured at K = 8192 in bf16 out; fp32 out takes about 1.7 times as long in all.
-// The small tiles win while they fit one round, since each then has a CU to
-// itself and its stages wait on memory, not on the matrix unit; e.g. N = 4096,
-// K = 8192, us (32x64 / 64x64 / 64x128 / 128x128 / 128x256 / 256x256):
-//   128 rows  23 / 25 / 28 / 36 / 53 / 72      512 rows  51 / 34 / 31 / 37 / 54 / 87
-//   2048 rows 205 / 131 / 119 / 82 / 71 / 99   4096 rows - / - / - / - / 155 / 126
+// The tiles: rows, weight rows, and what one block of K takes in ns: in the
+// first round of workgroups, and in each further one (the 32 x 64 ones share a CU
+// with others, so their further rounds overlap). `one`: for a single round
+// only, with stages of several blocks. Measured at K = 8192 in bf16 out; fp32 out
+// takes about 1.7 times as long in all. Small tiles win while they fit one
+// round: each has a CU to itself, and its stages wait on memory and on each
+// other, not on the matrix unit. N = 4096, K = 8192, us:
+//   rows   32x64 one  64x64 one  64x128 one  32x64  64x128  128x128  128x256  256x256
+//    128       15        18          23        22      28       35       53       71
+//    256       29        20          24        30      29       36       53       88
+//    512       53        36          27        50      31       37       54       88
+//   2048        -         -           -       204     119       82       71       99
+//   4096        -         -           -         -       -        -      155      124
 struct TileShape {
   int rows, cols, first_ns, more_ns;
+  bool one;
 };
-constexpr TileShape kTiles[] = {{32, 64, 340, 210},   {64, 64, 390, 260},   {64, 128, 450, 450},
-                                {128, 128, 620, 620}, {128, 256, 1100, 1100}, {256, 256, 1800, 1800}};
+constexpr TileShape kTiles[] = {{32, 64, 230, 0, true},       {64, 64, 300, 0, true},       {64, 128, 420, 0, true},
+                                {32, 64, 340, 210, false},    {64, 128, 450, 450, false},   {128, 128, 620, 620, false},
+                                {128, 256, 1100, 1100, false}, {256, 256, 1800, 1800, false}};
+constexpr int kNTiles = 8;
 
 int best_tile(const Fp8Gemm& g) {
   // rows of one group: experts get theirs unevenly, by about the root of the mean
   const double mean = static_cast<double>(g.rows) / g.experts;
   const double rows = g.experts > 1 ? mean + std::sqrt(mean) : mean;
   const int groups = std::min(g.rows, g.experts);
-  int best = 0;
-  double least = 0.0;
-  for (int i = 0; i < 6; ++i) {
+  int best = 3;
+  double least = 1e30;
+  for (int i = 0; i < kNTiles; ++i) {
     const TileShape& t = kTiles[i];
     // 256 x 256: its sums fill the registers, no room for bf16 operands; and
     // partly filled ones waste most (experts of 128 rows: 1153 us against 1051)
     if (t.rows == 256 && (g.f32 || (g.experts > 1 && mean < 512))) continue;
     const double tiles = groups * std::ceil(rows / t.rows) * std::ceil(static_cast<double>(g.N) / t.cols);
+    if (t.one && tiles > 256.0) continue;
     const double rounds = t.more_ns == t.first_ns ? std::ceil(tiles / 256.0) : std::max(1.0, tiles / 256.0);
     const double ns = t.first_ns + (rounds - 1.0) * t.more_ns;
-    if (i == 0 || ns < least) {
+    if (ns < least) {
       least = ns;
       best = i;
     }
@@ -672,12 +715,16 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t st) {
   // 8192, K = 4096 18 against 13)
   if (g.experts == 1 && g.rows <= 32 && g.N <= g.K) return launch_stream<2, 2>(g, groups, st);
   switch (best_tile(g)) {
-    case 0: return launch_tile<1, 4, 2, 1, 4>(g, st);
-    case 1: return launch_tile<2, 2, 2, 2, 4>(g, st);
-    case 2: return launch_tile<2, 4, 2, 2, 4>(g, st);
-    case 3: return launch_tile<2, 4, 4, 2, 4>(g, st);
-    case 4: return launch_tile<2, 4, 4, 4, 3>(g, st);
-    default: return launch_tile_as<2, 4, 8, 4, 2, false>(g, st);
+    // (four blocks per stage where their decoding is the longer part: 33 rows in
+    // fp32, N = 8192, K = 4096, 12.4 us against 13.6; bf16 11.0 against 10.5)
+    case 0: return g.f32 ? launch_tile_as<1, 4, 2, 1, 3, 4, true>(g, st) : launch_tile_as<1, 4, 2, 1, 4, 2, false>(g, st);
+    case 1: return launch_tile<2, 2, 2, 2, 3, 2>(g, st);
+    case 2: return launch_tile<2, 4, 2, 2, 3, 2>(g, st);
+    case 3: return launch_tile<1, 4, 2, 1, 4, 1>(g, st);
+    case 4: return launch_tile<2, 4, 2, 2, 4, 1>(g, st);
+    case 5: return launch_tile<2, 4, 4, 2, 4, 1>(g, st);
+    case 6: return launch_tile<2, 4, 4, 4, 3, 1>(g, st);
+    default: return launch_tile_as<2, 4, 8, 4, 2, 1, false>(g, st);
   }
 }
 

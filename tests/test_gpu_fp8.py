@@ -161,7 +161,7 @@ def test_linear(rows, n, k, dtype):
 
 
 # (rows, n, k) that fill the chip with each tile size, with ragged rows, weight rows and blocks of K
-WIDE = [(30, 9000, 400), (70, 8200, 1040), (200, 4100, 400), (300, 5000, 272), (500, 4200, 1168), (520, 8200, 144),
+WIDE = [(30, 9000, 400), (70, 8200, 1040), (200, 4000, 1040), (200, 4100, 400), (5, 20000, 528), (9, 65536, 144), (300, 5000, 272), (500, 4200, 1168), (520, 8200, 144),
         (1030, 8200, 144), (2100, 4200, 528), (2300, 8200, 256), (511, 20001, 144)]
 
 
@@ -185,6 +185,20 @@ def test_grouped_wide(experts, mean, n, k, dtype):
     sizes = (part / part.sum() * mean * experts).round().int().tolist()
     bounds = [0] + torch.tensor(sizes).cumsum(0).tolist()
     x, xs, w, ws = dev(*operands(bounds[-1], n, k, g, experts))
+    got = B.fp8_grouped(x, xs, torch.tensor(bounds, dtype=torch.int32).cuda(), w, ws, dtype)
+    check_grouped(got, x, xs, w, ws, bounds)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,k", [(9000, 400), (4100, 1040), (2080, 272), (300, 2064)])
+def test_grouped_few_rows_wide(n, k, dtype):
+    """A token's routes: one or two rows on a few of the experts, K split between fewer and more wavefronts."""
+    g = gen(n)
+    sizes = [0] * 40
+    for e in (0, 3, 4, 9, 20, 31, 38, 39):
+        sizes[e] = 1 + (e == 9)
+    bounds = [0] + torch.tensor(sizes).cumsum(0).tolist()
+    x, xs, w, ws = dev(*operands(bounds[-1], n, k, g, 40))
     got = B.fp8_grouped(x, xs, torch.tensor(bounds, dtype=torch.int32).cuda(), w, ws, dtype)
     check_grouped(got, x, xs, w, ws, bounds)
 
