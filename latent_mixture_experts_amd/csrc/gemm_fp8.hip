@@ -168,19 +168,19 @@ __device__ __forceinline__ void store4(const Fp8Gemm& p, int row, int n, f32x4 v
 }
 
 // ---- few rows: the weights stream once from HBM ----------------------------
-// A wavefront takes 16 weight rows x up to 16 * F rows over a run of K's
-// blocks; KS wavefronts of a workgroup split K and are joined through LDS in
-// order, and the workgroup's 8 / KS such teams take neighbouring weight rows.
-// Everything a block needs (codes of both operands, scales) is loaded to
-// registers D blocks ahead, so each wavefront keeps D * 2 KiB of weights in
-// flight and waits for nothing else. A group of more rows takes them in
-// passes. Grid: (weight row tiles, groups).
+// A wavefront takes 16 weight rows x up to 16 rows over a run of K's blocks;
+// KS wavefronts of a workgroup split K and are joined through LDS in order, and
+// the workgroup's 8 / KS such teams take neighbouring weight rows. Everything a
+// block needs (codes of both operands, scales) is loaded to registers D blocks
+// ahead, so each wavefront keeps D * 2 KiB of weights in flight and waits for
+// nothing else. A group of more rows takes them in passes. Grid: (weight row
+// tiles, groups).
 constexpr int kFW = 8;  // wavefronts
 
-template <int F, int KS, int D, bool F32>
-__global__ __launch_bounds__(64 * kFW, F <= 2 ? 4 : 2) void fp8_stream_kernel(Fp8Gemm p) {
+template <int KS, int D, bool F32>
+__global__ __launch_bounds__(64 * kFW, 4) void fp8_stream_kernel(Fp8Gemm p) {
   constexpr int kTeams = kFW / KS;
-  __shared__ f32x4 part[KS > 1 ? kFW : 1][F][64];
+  __shared__ f32x4 part[KS > 1 ? kFW : 1][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nl = lane & 15, g = lane >> 4;
   const Group grp = p.offsets ? find_group(p, static_cast<int>(blockIdx.y), 1 << 30) : Group{0, 0, p.rows};
@@ -200,30 +200,25 @@ __global__ __launch_bounds__(64 * kFW, F <= 2 ? 4 : 2) void fp8_stream_kernel(Fp
   const uint32_t w_off = static_cast<uint32_t>(nl) * p.K + g * 16;
   // Wavefronts that take all of K start at different blocks: weight rows lie a
   // power of two apart as a rule, and wavefronts that walk them in step meet on
-  // the same memory channels (32 verified tokens' down projection 557 -> 510 us).
+  // the same memory channels (8 tokens' down projection 213 -> 193 us).
   const int turn =
       KS == 1 ? __builtin_amdgcn_readfirstlane((5 * (static_cast<int>(blockIdx.x) + wave) + static_cast<int>(blockIdx.y)) % nkb) : 0;
 
-  for (int r0 = grp.begin; r0 < grp.end; r0 += 16 * F) {
+  for (int r0 = grp.begin; r0 < grp.end; r0 += 16) {
     const int base = p.index ? 0 : r0;  // the descriptors start at this row of x
-    const int xrows = p.index ? p.x_rows : min(grp.end - r0, 16 * F);
+    const int xrows = p.index ? p.x_rows : min(grp.end - r0, 16);
     const rsrc_t x_r = make_rsrc(p.x + static_cast<size_t>(base) * p.ldx,
                                  static_cast<uint32_t>(static_cast<size_t>(xrows - 1) * p.ldx + K));
     const rsrc_t xs_r = make_rsrc(p.xs + static_cast<size_t>(base) * nkb, static_cast<uint32_t>(xrows) * nkb * 4u);
-    uint32_t x_off[F], xs_off[F];  // (lanes without a row read nothing)
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      const int r = r0 + f * 16 + nl;
-      const int src = r < grp.end ? source_row(p, r) - base : 0;
-      x_off[f] = r < grp.end ? static_cast<uint32_t>(src * p.ldx) + g * 16 : kOutOfRange;
-      xs_off[f] = r < grp.end ? static_cast<uint32_t>(src) * nkb * 4u : kOutOfRange;
-    }
-    f32x4 acc[F];
-#pragma unroll
-    for (int f = 0; f < F; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // (lanes without a row read nothing)
+    const int row = r0 + nl;
+    const int src = row < grp.end ? source_row(p, row) - base : 0;
+    const uint32_t x_off = row < grp.end ? static_cast<uint32_t>(src * p.ldx) + g * 16 : kOutOfRange;
+    const uint32_t xs_off = row < grp.end ? static_cast<uint32_t>(src) * nkb * 4u : kOutOfRange;
+    f32x4 acc{0.f, 0.f, 0.f, 0.f};
 
-    uint4 wv[D][2], xv[D][F][2];
-    float xsv[D][F], wsv[D];
+    uint4 wv[D][2], xv[D][2];
+    float xsv[D], wsv[D];
     auto load = [&](int u, int i) __attribute__((always_inline)) {
       const int turned = i + turn;
       const int kb = kb0 + (turned >= n_kb ? turned - n_kb : turned);
@@ -232,24 +227,19 @@ __global__ __launch_bounds__(64 * kFW, F <= 2 ? 4 : 2) void fp8_stream_kernel(Fp
       for (int h = 0; h < 2; ++h) {  // (pieces past the last value: zeros in both operands)
         const bool in = static_cast<int>(at) + h * 64 + g * 16 < p.K;
         wv[u][h] = buf_load16<kAuxStream>(w_r, in ? w_off + at + h * 64 : kOutOfRange);
-#pragma unroll
-        for (int f = 0; f < F; ++f) xv[u][f][h] = buf_load16<kAuxDefault>(x_r, in ? x_off[f] + at + h * 64 : kOutOfRange);
+        xv[u][h] = buf_load16<kAuxDefault>(x_r, in ? x_off + at + h * 64 : kOutOfRange);
       }
-#pragma unroll
-      for (int f = 0; f < F; ++f) xsv[u][f] = __uint_as_float(buf_load4<kAuxDefault>(xs_r, xs_off[f] + kb * 4));
+      xsv[u] = __uint_as_float(buf_load4<kAuxDefault>(xs_r, xs_off + kb * 4));
       wsv[u] = __uint_as_float(buf_load4<kAuxDefault>(ws_r, kb * 4));
     };
     auto consume = [&](int u) __attribute__((always_inline)) {
       Operand<true> wf, xf;
       wf.set(pair16(wv[u][0], wv[u][1]));
+      xf.set(pair16(xv[u][0], xv[u][1]));
+      const f32x4 d = mfma_block(wf, xf);
+      const float s = xsv[u] * wsv[u];
 #pragma unroll
-      for (int f = 0; f < F; ++f) {
-        xf.set(pair16(xv[u][f][0], xv[u][f][1]));
-        const f32x4 d = mfma_block(wf, xf);
-        const float s = xsv[u][f] * wsv[u];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[f][i] = fmaf(d[i], s, acc[f][i]);
-      }
+      for (int i = 0; i < 4; ++i) acc[i] = fmaf(d[i], s, acc[i]);
     };
 #pragma unroll
     for (int u = 0; u < D; ++u)
@@ -274,21 +264,14 @@ __global__ __launch_bounds__(64 * kFW, F <= 2 ? 4 : 2) void fp8_stream_kernel(Fp
       if (i + u < n_kb) consume(u);
 
     if constexpr (KS == 1) {
-#pragma unroll
-      for (int f = 0; f < F; ++f) {
-        const int r = r0 + f * 16 + nl;
-        if (r < grp.end && n0 + 4 * g < p.N) store4<F32>(p, r, n0 + 4 * g, acc[f]);
-      }
+      if (row < grp.end && n0 + 4 * g < p.N) store4<F32>(p, row, n0 + 4 * g, acc);
     } else {
-#pragma unroll
-      for (int f = 0; f < F; ++f) part[wave][f][lane] = acc[f];
+      part[wave][lane] = acc;
       __syncthreads();
-      for (int f = ks; f < F; f += KS) {
-        f32x4 s = part[wave - ks][f][lane];
+      if (ks == 0) {
 #pragma unroll
-        for (int v = 1; v < KS; ++v) s += part[wave - ks + v][f][lane];
-        const int r = r0 + f * 16 + nl;
-        if (r < grp.end && n0 + 4 * g < p.N) store4<F32>(p, r, n0 + 4 * g, s);
+        for (int v = 1; v < KS; ++v) acc += part[wave + v][lane];
+        if (row < grp.end && n0 + 4 * g < p.N) store4<F32>(p, row, n0 + 4 * g, acc);
       }
       __syncthreads();  // (the next pass writes part again)
     }
@@ -321,7 +304,7 @@ __device__ __forceinline__ uint32_t lds_address(const T* p) {
 }
 
 template <int WT, int WW, int FT, int FW, int R, int KG, bool F32>
-__global__ __launch_bounds__(64 * WT * WW * KG) void fp8_tile_kernel(Fp8Gemm p, int n_row_tiles, int n_col_tiles) {
+__global__ __launch_bounds__(64 * WT * WW * KG) void fp8_tile_kernel(Fp8Gemm p, int n_row_tiles, int n_col_tiles, int chunk) {
   constexpr int kGroup = WT * WW, NW = kGroup * KG, BM = WT * FT * 16, BN = WW * FW * 16;
   constexpr int kXOps = BM / 8 / kGroup, kWOps = BN / 8 / kGroup;  // 1-KiB copies per wavefront and stage (its group's block)
   constexpr int kFSet = KG == 1 ? 4 : KG;                          // blocks of a scale set
@@ -344,8 +327,8 @@ __global__ __launch_bounds__(64 * WT * WW * KG) void fp8_tile_kernel(Fp8Gemm p, 
   const int kg = wave / kGroup, wt = wave % kGroup % WT, ww = wave % kGroup / WT;
 
   int mt, nt;
-  if (p.offsets) {  // an expert's row tiles share its weights in one XCD's L2
-    const int logical = xcd_tile(2 * n_col_tiles);
+  if (p.offsets) {
+    const int logical = xcd_tile(chunk);
     mt = logical / n_col_tiles;
     nt = logical % n_col_tiles;
   } else {
@@ -611,13 +594,13 @@ __global__ __launch_bounds__(64 * WT * WW * KG) void fp8_tile_kernel(Fp8Gemm p, 
   }
 }
 
-template <int F, int KS, int D>
+template <int KS, int D>
 hipError_t launch_stream_ks(const Fp8Gemm& g, int tiles, int groups, hipStream_t st) {
   const dim3 grid((tiles * KS + kFW - 1) / kFW, groups), block(64 * kFW);
   if (g.f32)
-    MOE_LAUNCH((fp8_stream_kernel<F, KS, D, true>), grid, block, 0, st, g);
+    MOE_LAUNCH((fp8_stream_kernel<KS, D, true>), grid, block, 0, st, g);
   else
-    MOE_LAUNCH((fp8_stream_kernel<F, KS, D, false>), grid, block, 0, st, g);
+    MOE_LAUNCH((fp8_stream_kernel<KS, D, false>), grid, block, 0, st, g);
   return hipGetLastError();
 }
 
@@ -625,28 +608,33 @@ hipError_t launch_stream_ks(const Fp8Gemm& g, int tiles, int groups, hipStream_t
 // token's gate/up, 8 experts x 512 tiles: no split 57 us, split by two 59);
 // a wavefront with all of K keeps four blocks in flight, one with a part two
 // (one pooler token 9.3 -> 8.8 us, fewer registers).
-template <int F, int D>
 hipError_t launch_stream(const Fp8Gemm& g, int groups, hipStream_t st) {
   const int tiles = (g.N + 15) / 16;
   const int64_t waves = static_cast<int64_t>(tiles) * groups;
-  if (waves >= 4096) return launch_stream_ks<F, 1, D>(g, tiles, groups, st);
-  if (waves >= 2048) return launch_stream_ks<F, 2, 2>(g, tiles, groups, st);
-  if (waves >= 1024) return launch_stream_ks<F, 4, 2>(g, tiles, groups, st);
-  return launch_stream_ks<F, 8, 2>(g, tiles, groups, st);
+  if (waves >= 4096) return launch_stream_ks<1, 4>(g, tiles, groups, st);
+  if (waves >= 2048) return launch_stream_ks<2, 2>(g, tiles, groups, st);
+  if (waves >= 1024) return launch_stream_ks<4, 2>(g, tiles, groups, st);
+  return launch_stream_ks<8, 2>(g, tiles, groups, st);
 }
 
 template <int WT, int WW, int FT, int FW, int R, int KG, bool F32>
 hipError_t launch_tile_as(const Fp8Gemm& g, hipStream_t st) {
   constexpr int BM = WT * FT * 16, BN = WW * FW * 16;
   const int nct = (g.N + BN - 1) / BN;
-  int nrt = (g.rows + BM - 1) / BM, grid;
+  int nrt = (g.rows + BM - 1) / BM, grid, chunk = 1;
   if (g.offsets) {
     nrt = g.rows / BM + std::min(g.rows, g.experts);  // every expert may end in a partial tile
-    grid = xcd_grid(nrt * nct, 2 * nct);
+    // Tiles dealt to the XCDs: with an expert in one or two row tiles, both with
+    // all their column tiles to one XCD, so that its weights enter one L2. With
+    // more, or too few to go round, single tiles: a column tile then meets the
+    // same XCD for every row tile as a rule (2000 tokens on 16 experts 206 ->
+    // 196 us, one token's 8 routes 38 -> 26).
+    if (nrt > 32 && g.rows < static_cast<int64_t>(2 * BM) * g.experts) chunk = 2 * nct;
+    grid = xcd_grid(nrt * nct, chunk);
   } else {
     grid = (nrt * nct + 7) / 8 * 8;
   }
-  MOE_LAUNCH((fp8_tile_kernel<WT, WW, FT, FW, R, KG, F32>), dim3(grid), dim3(64 * WT * WW * KG), 0, st, g, nrt, nct);
+  MOE_LAUNCH((fp8_tile_kernel<WT, WW, FT, FW, R, KG, F32>), dim3(grid), dim3(64 * WT * WW * KG), 0, st, g, nrt, nct, chunk);
   return hipGetLastError();
 }
 template <int WT, int WW, int FT, int FW, int R, int KG>
@@ -706,14 +694,14 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t st) {
   const int groups = std::min(g.rows, g.experts);
   const int mean = (g.rows - 1) / g.experts + 1;
   // Few rows and little to stream: the streaming kernel (one pooler token 9 us
-  // against 18 with 32 x 64 tiles, one token's gate/up 57 against 72). Where
-  // the tiles fill the chip several times over they read faster, whole
-  // 128-byte lines at a time (32 tokens' down projection 481 us against 510).
-  if (g.rows <= 64 && mean <= 16 && static_cast<int64_t>(groups) * ((g.N + 63) / 64) < 2048)
-    return launch_stream<1, 4>(g, groups, st);
-  // (17 .. 32 rows, deep and narrow: N = 4096, K = 8192 17 us against 21; N =
-  // 8192, K = 4096 18 against 13)
-  if (g.experts == 1 && g.rows <= 32 && g.N <= g.K) return launch_stream<2, 2>(g, groups, st);
+  // against 13 with tiles, 16 tokens 12.3 against 13.3; 8 tokens on 4 experts
+  // 12.8 against 12.0 .. 13.0). Where the tiles fill the chip they read faster,
+  // whole 128-byte lines at a time (32 tokens' down projection 480 us against
+  // 510), and dense from 8192 weight rows on (N = 8192, K = 4096: 4 rows 9.3
+  // against 9.8, 16 rows 9.5 against 12.6).
+  if (g.rows <= 64 && mean <= 16 && static_cast<int64_t>(groups) * ((g.N + 63) / 64) < 2048 &&
+      !(g.experts == 1 && g.N >= 8192 && g.rows > 4))
+    return launch_stream(g, groups, st);
   switch (best_tile(g)) {
     // (four blocks per stage where their decoding is the longer part: 33 rows in
     // fp32, N = 8192, K = 4096, 12.4 us against 13.6; bf16 11.0 against 10.5)
