@@ -42,7 +42,8 @@
  * Supported shapes (else MOE_EUNSUPPORTED): hidden, latent and inter are
  * multiples of 128, at least 128, latent <= 8192, hidden and inter <= 65536;
  * 1 <= n_experts <= 256; 1 <= top_k <= min(8, n_experts);
- * T * top_k < 2^28. Pointers must be 16-byte aligned (MOE_EALIGN).
+ * T * top_k < 2^28. Pointers must be 16-byte aligned (MOE_EALIGN), unless an
+ * entry point states another alignment.
  */
 #ifndef MOE_H
 #define MOE_H
@@ -57,7 +58,7 @@ extern "C" {
 #define MOE_OK 0
 #define MOE_EINVAL (-1)       /* null pointer, negative size, bad eps or flag   */
 #define MOE_EUNSUPPORTED (-2) /* dims outside the supported shapes above        */
-#define MOE_EALIGN (-3)       /* a pointer is not 16-byte aligned               */
+#define MOE_EALIGN (-3)       /* a pointer (or row pitch) is not aligned, 16 bytes unless stated otherwise */
 #define MOE_EWORKSPACE (-4)   /* workspace smaller than moe_workspace_bytes()   */
 #define MOE_EHIP (-5)         /* a HIP launch failed (see moe_last_hip_error)   */
 

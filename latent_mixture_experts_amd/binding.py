@@ -280,7 +280,8 @@ def workspace_view(d: MoeDims, T: int, ws: torch.Tensor, which: str, dtype, shap
 # ---- 8-bit rows, their products, the balance loss --------------------------
 # These take their sizes from the tensors, so they check them: a wrong shape,
 # type, layout or device raises ValueError before anything is enqueued. They
-# run on the tensors' device, on its current stream unless one is given.
+# run on the tensors' device, on its current stream unless one is given (a
+# torch.cuda.Stream; what they allocate then belongs to that stream).
 TYPE_BF16, TYPE_F32 = 0, 1  # MOE_TYPE_*
 _FLOATS = {torch.bfloat16: TYPE_BF16, torch.int16: TYPE_BF16, torch.float32: TYPE_F32}  # int16: bf16 bits
 _CODES = (torch.float8_e4m3fn, torch.uint8)
@@ -322,6 +323,15 @@ def _run(what: str, dev: torch.device, stream, *args) -> None:
         raise MoeError(rc, what)
 
 
+def _empty(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
+    """A tensor of the stream that the call runs on: memory of another stream's
+    pool could still be in use there, or be handed out again before the call is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _device(t: torch.Tensor) -> torch.device:
     _need(t.is_cuda, "the tensors must be on a GPU")
     return t.device
@@ -332,11 +342,11 @@ def _quantize(what: str, x: torch.Tensor, cols: int, codes, scales, stream):
     rows = x.shape[0]
     _check("x", x, dev, tuple(_FLOATS), (rows, x.shape[1]), pitched=True)
     if codes is None:
-        codes = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
+        codes = _empty((rows, cols), torch.float8_e4m3fn, dev, stream)
     else:
         _check("codes", codes, dev, _CODES, (rows, cols))
     if scales is None:
-        scales = torch.empty((rows, _blocks(cols)), dtype=torch.float32, device=dev)
+        scales = _empty((rows, _blocks(cols)), torch.float32, dev, stream)
     else:
         _check("scales", scales, dev, (torch.float32,), (rows, _blocks(cols)))
     _run(what, dev, stream, rows, cols, x.data_ptr(), _pitch(x), _FLOATS[x.dtype], codes.data_ptr(),
@@ -358,10 +368,10 @@ def fp8_swiglu(gate_up: torch.Tensor, codes=None, scales=None, stream=None):
     return _quantize("moe_fp8_swiglu", gate_up, gate_up.shape[1] // 2, codes, scales, stream)
 
 
-def _out(out, rows: int, n: int, dtype, dev: torch.device) -> torch.Tensor:
+def _out(out, rows: int, n: int, dtype, dev: torch.device, stream) -> torch.Tensor:
     if out is None:
         _need(dtype in _FLOATS, f"out_dtype: bfloat16 or float32, got {dtype}")
-        return torch.empty((rows, n), dtype=dtype, device=dev)
+        return _empty((rows, n), dtype, dev, stream)
     _check("out", out, dev, tuple(_FLOATS), (rows, n), pitched=True)
     return out
 
@@ -378,7 +388,7 @@ def fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     _check("x_scales", x_scales, dev, (torch.float32,), (T, _blocks(K)))
     _check("w", w, dev, _CODES, (N, K))
     _check("w_scales", w_scales, dev, (torch.float32,), (_blocks(N), _blocks(K)))
-    out = _out(out, T, N, out_dtype, dev)
+    out = _out(out, T, N, out_dtype, dev, stream)
     _run("moe_fp8_linear", dev, stream, T, N, K, x.data_ptr(), _pitch(x), x_scales.data_ptr(),
          w.data_ptr(), w_scales.data_ptr(), out.data_ptr(), _pitch(out), _FLOATS[out.dtype])
     return out
@@ -403,7 +413,7 @@ def fp8_grouped(x: torch.Tensor, x_scales: torch.Tensor, offsets: torch.Tensor, 
     if row_index is not None:
         rows = row_index.numel()
         _check("row_index", row_index, dev, (torch.int32,), (rows,))
-    out = _out(out, rows, N, out_dtype, dev)
+    out = _out(out, rows, N, out_dtype, dev, stream)
     _run("moe_fp8_grouped", dev, stream, rows, E, N, K, offsets.data_ptr(), _ptr(row_index), index_div,
          x_rows, x.data_ptr(), _pitch(x), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
          out.data_ptr(), _pitch(out), _FLOATS[out.dtype])
@@ -428,11 +438,11 @@ def balance_loss(logits: torch.Tensor, ids: torch.Tensor, mask=None, ws=None, st
         _check("mask", mask, dev, (torch.uint8, torch.bool), (T,))
     if ws is None:
         n = balance_workspace_bytes(T, E)
-        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        ws = _empty(n, torch.uint8, dev, stream) if n else None
     else:
         _check("ws", ws, dev, (torch.uint8,), (ws.numel(),))
-    losses = torch.empty(2, dtype=torch.float32, device=dev)
-    counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    losses = _empty(2, torch.float32, dev, stream)
+    counts = _empty(E + 1, torch.int32, dev, stream)
     _run("moe_balance_loss", dev, stream, T, E, K, logits.data_ptr(), ids.data_ptr(), _ptr(mask),
          counts.data_ptr(), losses.data_ptr(), _ptr(ws), ws.numel() if ws is not None else 0)
     return losses, counts
@@ -460,7 +470,7 @@ def balance_loss_backward(logits: torch.Tensor, ids: torch.Tensor, counts: torch
         _check("w", w, dev, f32, (T, K))
         _check("grad_w", grad_w, dev, f32, (T, K))
     if out is None:
-        out = torch.empty((T, E), dtype=torch.float32, device=dev)
+        out = _empty((T, E), torch.float32, dev, stream)
     else:
         _check("out", out, dev, f32, (T, E))
     _run("moe_balance_loss_backward", dev, stream, T, E, K, logits.data_ptr(), ids.data_ptr(), _ptr(mask),

@@ -745,7 +745,7 @@ const char* moe_status_string(int status) {
     case MOE_OK: return "ok";
     case MOE_EINVAL: return "invalid argument (null pointer, negative size, bad eps or flag)";
     case MOE_EUNSUPPORTED: return "unsupported dimensions";
-    case MOE_EALIGN: return "pointer not 16-byte aligned";
+    case MOE_EALIGN: return "pointer or row pitch not aligned (16 bytes unless stated otherwise)";
     case MOE_EWORKSPACE: return "workspace too small";
     case MOE_EHIP: return "HIP launch failed";
     default: return "unknown status";

@@ -206,6 +206,25 @@ def test_loss_from_the_router():
     check_grad(got, grad, size)
 
 
+def test_a_given_stream():
+    """A call on a stream of its own, its workspace and results allocated
+    there, while the current stream frees and takes memory."""
+    logits, ids, w, dw, mask = (cuda(t) for t in case(20000, 256, 8, True))
+    gl = torch.tensor([0.3, 0.1], device="cuda")
+    want = B.balance_loss(logits, ids, mask)
+    want_g = B.balance_loss_backward(logits, ids, want[1], gl, mask, w, dw)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(6):
+        losses, counts = B.balance_loss(logits, ids, mask, stream=s)
+        got.append((losses, counts, B.balance_loss_backward(logits, ids, counts, gl, mask, w, dw, stream=s)))
+        torch.full((1 << 18,), 7.0, device="cuda")
+    s.synchronize()
+    for losses, counts, g in got:
+        assert torch.equal(losses, want[0]) and torch.equal(counts, want[1]) and torch.equal(g, want_g)
+
+
 def test_refusals():
     logits, ids, w, dw, mask = (cuda(t) for t in case(70, 8, 2, True))
     counts = torch.zeros(9, dtype=torch.int32, device="cuda")
