@@ -306,16 +306,19 @@ __device__ __forceinline__ uint32_t lds_address(const T* p) {
 template <int WT, int WW, int FT, int FW, int R, int KG, bool F32>
 __global__ __launch_bounds__(64 * WT * WW * KG) void fp8_tile_kernel(Fp8Gemm p, int n_row_tiles, int n_col_tiles, int chunk) {
   constexpr int kGroup = WT * WW, NW = kGroup * KG, BM = WT * FT * 16, BN = WW * FW * 16;
-  constexpr int kXOps = BM / 8 / kGroup, kWOps = BN / 8 / kGroup;  // 1-KiB copies per wavefront and stage (its group's block)
+  // 1-KiB copies per wavefront and stage (its group's block); of the rows' some
+  // wavefronts may have one fewer
+  constexpr int kXOps = (BM / 8 + kGroup - 1) / kGroup, kXLeast = BM / 8 / kGroup, kWOps = BN / 8 / kGroup;
   constexpr int kFSet = KG == 1 ? 4 : KG;                          // blocks of a scale set
   constexpr int kSetRows = 64 / kFSet, kSets = KG == 1 ? 2 : R;    // rows of one 64-scale copy; sets held
   constexpr int kSOps = (BM / kSetRows + NW - 1) / NW;             // such copies per wavefront and set
   static_assert((BN % kFp8Block == 0 || kFp8Block % BN == 0) && BN * kFSet <= 64 * kFp8Block, "tiles within weight blocks");
-  static_assert(kXOps * 8 * kGroup == BM && kWOps * 8 * kGroup == BN && BM % kSetRows == 0, "whole copies");
-  constexpr int kOps = kXOps + kWOps;
-  static_assert((R - 2) * kOps < 64, "vmcnt field");
+  static_assert(kWOps * 8 * kGroup == BN && BM % kSetRows == 0 && kXLeast > 0, "whole copies");
+  constexpr int kOps = kXOps + kWOps, kLeast = kXLeast + kWOps;
+  static_assert((R - 2) * kLeast < 64, "vmcnt field");
   // (KG = 1: a set is asked for four stages before its first use, and the wait
-  // of the third of them leaves the copies of R - 2 stages outstanding, all younger)
+  // of the third of them leaves at most the copies of R - 2 stages outstanding,
+  // all younger)
   static_assert(R >= 2 && R <= 4, "scale sets land in time");
   constexpr int kXSlot = KG * BM * kFp8Block, kWSlot = KG * BN * kFp8Block;  // bytes of a stage
   __shared__ __attribute__((aligned(1024))) uint8_t Xs[R][kXSlot];
@@ -361,12 +364,12 @@ __global__ __launch_bounds__(64 * WT * WW * KG) void fp8_tile_kernel(Fp8Gemm p, 
   uint32_t xoff[kXOps], woff[kWOps], soff[kSOps];
 #pragma unroll
   for (int i = 0; i < kXOps; ++i) {
-    const int r = (kXOps * (wave % kGroup) + i) * 8 + (lane >> 3), src = row_of(r);
+    const int r = (i * kGroup + wave % kGroup) * 8 + (lane >> 3), src = row_of(r);
     xoff[i] = src < 0 ? kOutOfRange : static_cast<uint32_t>(src * p.ldx) + kg * kFp8Block + ((lane & 7) ^ ((r >> 1) & 7)) * 16;
   }
 #pragma unroll
   for (int i = 0; i < kWOps; ++i) {
-    const int r = (kWOps * (wave % kGroup) + i) * 8 + (lane >> 3);
+    const int r = (i * kGroup + wave % kGroup) * 8 + (lane >> 3);
     woff[i] = static_cast<uint32_t>(r) * p.K + kg * kFp8Block + ((lane & 7) ^ ((r >> 1) & 7)) * 16;
   }
 #pragma unroll
@@ -391,10 +394,10 @@ __global__ __launch_bounds__(64 * WT * WW * KG) void fp8_tile_kernel(Fp8Gemm p, 
       auto in = [&](int q) { return ((lane & 7) ^ (((q * 8 + (lane >> 3)) >> 1) & 7)) * 16 < left; };
 #pragma unroll
       for (int i = 0; i < kXOps; ++i)
-        if (!in(kXOps * (wave % kGroup) + i)) xoff[i] = kOutOfRange;
+        if (!in(i * kGroup + wave % kGroup)) xoff[i] = kOutOfRange;
 #pragma unroll
       for (int i = 0; i < kWOps; ++i)
-        if (!in(kWOps * (wave % kGroup) + i)) woff[i] = kOutOfRange;
+        if (!in(i * kGroup + wave % kGroup)) woff[i] = kOutOfRange;
     }
     const bool none = st >= nst;
     return Stage{make_rsrc(none ? x_base : x_base + k0, none ? 0 : x_bytes - k0),
@@ -402,12 +405,15 @@ __global__ __launch_bounds__(64 * WT * WW * KG) void fp8_tile_kernel(Fp8Gemm p, 
   };
   // this wavefront's copy c (0 .. kOps-1) of a stage
   auto copy = [&](const Stage& s, int c) __attribute__((always_inline)) {
-    if (c < kXOps)
-      lds_copy16(s.x, xoff[c < kXOps ? c : 0],
-                 __builtin_amdgcn_readfirstlane(lds_x + s.slot * kXSlot + (kXOps * wave + c) * 1024));
-    else
+    const int i = c < kXOps ? c : c - kXOps, q = i * kGroup + wave % kGroup;  // 8-row block of the tile
+    if (c < kXOps) {
+      if (kXOps == kXLeast || q < BM / 8)
+        lds_copy16(s.x, xoff[c < kXOps ? c : 0],
+                   __builtin_amdgcn_readfirstlane(lds_x + s.slot * kXSlot + kg * (BM * kFp8Block) + q * 1024));
+    } else {
       lds_copy16(s.w, woff[c < kXOps ? 0 : c - kXOps],
-                 __builtin_amdgcn_readfirstlane(lds_w + s.slot * kWSlot + (kWOps * wave + c - kXOps) * 1024));
+                 __builtin_amdgcn_readfirstlane(lds_w + s.slot * kWSlot + kg * (BN * kFp8Block) + q * 1024));
+    }
   };
   auto issue_set = [&](int set, int at) __attribute__((always_inline)) {
     const bool in = set * kFSet + lane % kFSet < nkb;
@@ -463,7 +469,7 @@ __global__ __launch_bounds__(64 * WT * WW * KG) void fp8_tile_kernel(Fp8Gemm p, 
     __syncthreads();
     // the copies of stage st + 1 have landed, in every wavefront
     auto meet = [&](int st, int slot) __attribute__((always_inline)) {
-      wait_vm_lds<(R - 2) * kOps>();
+      wait_vm_lds<(R - 2) * kLeast>();
       __syncthreads();
       if constexpr (KG > 1) issue_set(st + R, slot);
       ahead = stage_of(st + R, slot);
@@ -655,14 +661,17 @@ hipError_t launch_tile(const Fp8Gemm& g, hipStream_t st) {
 //    512       53        36          27        50      31       37       54       88
 //   2048        -         -           -       204     119       82       71       99
 //   4096        -         -           -         -       -        -      155      124
+// 144 x 256 stands for experts of about 128 rows, half of which would take a
+// second, nearly empty tile of 128 (4096 tokens' down projection 1115 -> 1053 us;
+// experts of 109 rows 1014 against 1011).
 struct TileShape {
   int rows, cols, first_ns, more_ns;
   bool one;
 };
 constexpr TileShape kTiles[] = {{32, 64, 230, 0, true},       {64, 64, 300, 0, true},       {64, 128, 420, 0, true},
                                 {32, 64, 340, 210, false},    {64, 128, 450, 450, false},   {128, 128, 620, 620, false},
-                                {128, 256, 1100, 1100, false}, {256, 256, 1800, 1800, false}};
-constexpr int kNTiles = 8;
+                                {128, 256, 1100, 1100, false}, {144, 256, 1200, 1200, false}, {256, 256, 1800, 1800, false}};
+constexpr int kNTiles = 9;
 
 int best_tile(const Fp8Gemm& g) {
   // rows of one group: experts get theirs unevenly, by about the root of the mean
@@ -712,6 +721,7 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t st) {
     case 4: return launch_tile<2, 4, 2, 2, 4, 1>(g, st);
     case 5: return launch_tile<2, 4, 4, 2, 4, 1>(g, st);
     case 6: return launch_tile<2, 4, 4, 4, 3, 1>(g, st);
+    case 7: return launch_tile<1, 8, 9, 2, 3, 1>(g, st);
     default: return launch_tile_as<2, 4, 8, 4, 2, 1, false>(g, st);
   }
 }
