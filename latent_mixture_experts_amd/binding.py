@@ -285,6 +285,8 @@ def workspace_view(d: MoeDims, T: int, ws: torch.Tensor, which: str, dtype, shap
 TYPE_BF16, TYPE_F32 = 0, 1  # MOE_TYPE_*
 _FLOATS = {torch.bfloat16: TYPE_BF16, torch.int16: TYPE_BF16, torch.float32: TYPE_F32}  # int16: bf16 bits
 _CODES = (torch.float8_e4m3fn, torch.uint8)
+_ANY_FLOAT = tuple(_FLOATS)
+_F32, _I32, _MASK = (torch.float32,), (torch.int32,), (torch.uint8, torch.bool)
 
 
 def _blocks(n: int) -> int:
@@ -298,7 +300,7 @@ def _need(ok: bool, what: str) -> None:
 
 def _check(name: str, t: torch.Tensor, dev: torch.device, types, shape, pitched: bool = False) -> None:
     """t is on dev, of one of the types, of that shape, and dense (pitched: its rows are, at any pitch)."""
-    if (t.device != dev or t.dtype not in types or t.shape != shape or
+    if (t.shape != shape or t.dtype not in types or t.device != dev or
             not (t.is_contiguous() or (pitched and (t.shape[1] == 1 or t.stride(1) == 1)
                                        and t.stride(0) >= t.shape[1]))):
         raise ValueError(f"{name}: needs {'rows' if pitched else 'a dense tensor'} {list(shape)} of "
@@ -311,10 +313,10 @@ def _pitch(t: torch.Tensor) -> int:
 
 
 def _run(what: str, dev: torch.device, stream, *args) -> None:
-    fn = getattr(lib(), what)
+    fn = getattr(_lib or lib(), what)
     # (the current stream's handle alone: building a torch.cuda.Stream costs as much as the launch)
     st = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
-    if dev.index == torch.cuda.current_device():
+    if dev.index == torch._C._cuda_getDevice():
         rc = fn(*args, st)
     else:
         with torch.cuda.device(dev):
@@ -333,14 +335,16 @@ def _empty(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
 
 
 def _device(t: torch.Tensor) -> torch.device:
-    _need(t.is_cuda, "the tensors must be on a GPU")
-    return t.device
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors must be on a GPU, got {dev}")
+    return dev
 
 
 def _quantize(what: str, x: torch.Tensor, cols: int, codes, scales, stream):
     dev = _device(x)
     rows = x.shape[0]
-    _check("x", x, dev, tuple(_FLOATS), (rows, x.shape[1]), pitched=True)
+    _check("x", x, dev, _ANY_FLOAT, (rows, x.shape[1]), pitched=True)
     if codes is None:
         codes = _empty((rows, cols), torch.float8_e4m3fn, dev, stream)
     else:
@@ -348,7 +352,7 @@ def _quantize(what: str, x: torch.Tensor, cols: int, codes, scales, stream):
     if scales is None:
         scales = _empty((rows, _blocks(cols)), torch.float32, dev, stream)
     else:
-        _check("scales", scales, dev, (torch.float32,), (rows, _blocks(cols)))
+        _check("scales", scales, dev, _F32, (rows, _blocks(cols)))
     _run(what, dev, stream, rows, cols, x.data_ptr(), _pitch(x), _FLOATS[x.dtype], codes.data_ptr(),
          scales.data_ptr())
     return codes, scales
@@ -370,9 +374,10 @@ def fp8_swiglu(gate_up: torch.Tensor, codes=None, scales=None, stream=None):
 
 def _out(out, rows: int, n: int, dtype, dev: torch.device, stream) -> torch.Tensor:
     if out is None:
-        _need(dtype in _FLOATS, f"out_dtype: bfloat16 or float32, got {dtype}")
+        if dtype not in _FLOATS:
+            raise ValueError(f"out_dtype: bfloat16 or float32, got {dtype}")
         return _empty((rows, n), dtype, dev, stream)
-    _check("out", out, dev, tuple(_FLOATS), (rows, n), pitched=True)
+    _check("out", out, dev, _ANY_FLOAT, (rows, n), pitched=True)
     return out
 
 
@@ -385,9 +390,9 @@ def fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     dev = _device(x)
     (T, K), N = x.shape, w.shape[0]
     _check("x", x, dev, _CODES, (T, K), pitched=True)
-    _check("x_scales", x_scales, dev, (torch.float32,), (T, _blocks(K)))
+    _check("x_scales", x_scales, dev, _F32, (T, _blocks(K)))
     _check("w", w, dev, _CODES, (N, K))
-    _check("w_scales", w_scales, dev, (torch.float32,), (_blocks(N), _blocks(K)))
+    _check("w_scales", w_scales, dev, _F32, (_blocks(N), _blocks(K)))
     out = _out(out, T, N, out_dtype, dev, stream)
     _run("moe_fp8_linear", dev, stream, T, N, K, x.data_ptr(), _pitch(x), x_scales.data_ptr(),
          w.data_ptr(), w_scales.data_ptr(), out.data_ptr(), _pitch(out), _FLOATS[out.dtype])
@@ -406,13 +411,13 @@ def fp8_grouped(x: torch.Tensor, x_scales: torch.Tensor, offsets: torch.Tensor, 
     (x_rows, K), (E, N, _) = x.shape, w.shape
     rows = x_rows
     _check("x", x, dev, _CODES, (x_rows, K), pitched=True)
-    _check("x_scales", x_scales, dev, (torch.float32,), (x_rows, _blocks(K)))
-    _check("offsets", offsets, dev, (torch.int32,), (E + 1,))
+    _check("x_scales", x_scales, dev, _F32, (x_rows, _blocks(K)))
+    _check("offsets", offsets, dev, _I32, (E + 1,))
     _check("w", w, dev, _CODES, (E, N, K))
-    _check("w_scales", w_scales, dev, (torch.float32,), (E, _blocks(N), _blocks(K)))
+    _check("w_scales", w_scales, dev, _F32, (E, _blocks(N), _blocks(K)))
     if row_index is not None:
         rows = row_index.numel()
-        _check("row_index", row_index, dev, (torch.int32,), (rows,))
+        _check("row_index", row_index, dev, _I32, (rows,))
     out = _out(out, rows, N, out_dtype, dev, stream)
     _run("moe_fp8_grouped", dev, stream, rows, E, N, K, offsets.data_ptr(), _ptr(row_index), index_div,
          x_rows, x.data_ptr(), _pitch(x), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
@@ -432,10 +437,10 @@ def balance_loss(logits: torch.Tensor, ids: torch.Tensor, mask=None, ws=None, st
     _need(logits.dim() == 2 and ids.dim() == 2, "logits, ids: need two dimensions")
     dev = _device(logits)
     (T, E), K = logits.shape, ids.shape[1]
-    _check("logits", logits, dev, (torch.float32,), (T, E))
-    _check("ids", ids, dev, (torch.int32,), (T, K))
+    _check("logits", logits, dev, _F32, (T, E))
+    _check("ids", ids, dev, _I32, (T, K))
     if mask is not None:
-        _check("mask", mask, dev, (torch.uint8, torch.bool), (T,))
+        _check("mask", mask, dev, _MASK, (T,))
     if ws is None:
         n = balance_workspace_bytes(T, E)
         ws = _empty(n, torch.uint8, dev, stream) if n else None
@@ -458,21 +463,20 @@ def balance_loss_backward(logits: torch.Tensor, ids: torch.Tensor, counts: torch
     _need(logits.dim() == 2 and ids.dim() == 2, "logits, ids: need two dimensions")
     dev = _device(logits)
     (T, E), K = logits.shape, ids.shape[1]
-    f32 = (torch.float32,)
-    _check("logits", logits, dev, f32, (T, E))
-    _check("ids", ids, dev, (torch.int32,), (T, K))
-    _check("counts", counts, dev, (torch.int32,), (E + 1,))
-    _check("grad_losses", grad_losses, dev, f32, (2,))
+    _check("logits", logits, dev, _F32, (T, E))
+    _check("ids", ids, dev, _I32, (T, K))
+    _check("counts", counts, dev, _I32, (E + 1,))
+    _check("grad_losses", grad_losses, dev, _F32, (2,))
     if mask is not None:
-        _check("mask", mask, dev, (torch.uint8, torch.bool), (T,))
+        _check("mask", mask, dev, _MASK, (T,))
     _need((w is None) == (grad_w is None), "w, grad_w: both or neither")
     if w is not None:
-        _check("w", w, dev, f32, (T, K))
-        _check("grad_w", grad_w, dev, f32, (T, K))
+        _check("w", w, dev, _F32, (T, K))
+        _check("grad_w", grad_w, dev, _F32, (T, K))
     if out is None:
         out = _empty((T, E), torch.float32, dev, stream)
     else:
-        _check("out", out, dev, f32, (T, E))
+        _check("out", out, dev, _F32, (T, E))
     _run("moe_balance_loss_backward", dev, stream, T, E, K, logits.data_ptr(), ids.data_ptr(), _ptr(mask),
          counts.data_ptr(), grad_losses.data_ptr(), _ptr(w), _ptr(grad_w), out.data_ptr())
     return out
