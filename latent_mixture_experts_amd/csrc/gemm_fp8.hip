@@ -49,12 +49,11 @@ __device__ __forceinline__ bf16x8 e4m3x8_to_bf16(int lo, int hi) {
   return bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-// D(16x16, fp32) = A(16x128, E4M3) * B(128x16, E4M3). Lane l supplies row
-// l%16 of A and column l%16 of B; the 32 bytes of lane group l/16 may be any
-// 32 of the block's 128 as long as both operands take the same ones, since
-// the block is summed whole. It receives D rows 4*(l/16) .. +3 of column l%16.
-// An operand fragment as the matrix instructions take it: the codes, or
-// (EXACT) their bf16 values, decoded once for all the products it enters.
+// An operand fragment, 16 rows x one block, as the matrix instructions take it:
+// the codes, or (EXACT) their bf16 values, decoded once for all the products it
+// enters. Lane l holds 32 bytes of row l%16; which 32 of the block's 128 lane
+// group l/16 holds is free as long as both operands agree, since the block is
+// summed whole.
 template <bool EXACT>
 struct Operand {
   i32x8 codes;
@@ -68,6 +67,8 @@ struct Operand<true> {
     for (int s = 0; s < 4; ++s) v[s] = e4m3x8_to_bf16(c[2 * s], c[2 * s + 1]);
   }
 };
+// D(16x16, fp32) = A(16x128) * B(128x16)^T: lane l receives rows 4*(l/16) .. +3
+// of A against row l%16 of B.
 __device__ __forceinline__ f32x4 mfma_block(const Operand<false>& a, const Operand<false>& b) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.codes, b.codes, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
