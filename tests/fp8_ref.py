@@ -2,6 +2,8 @@
 loss, on the host (the oracle of their GPU tests), and how far fp32 may be off."""
 from __future__ import annotations
 
+import math
+
 import torch
 
 U24 = 2.0 ** -24  # half a step of fp32, relative
@@ -118,7 +120,10 @@ def balance(logits, ids, mask=None, grad_losses=None, w=None, grad_w=None, count
         f = counts[:e].double() * e / (k * n)
     gb, gz = grad_losses.double()
     grad = gb / n * p * (f - (p @ f)[:, None]) + gz / n * 2 * lse[:, None] * p
-    size = gb.abs() / n * p * (f + (p @ f)[:, None]) + gz.abs() / n * 2 * lse.abs()[:, None] * p
+    # (lse is the largest logit plus the logarithm of a sum in [1, E]: in fp32 its
+    # error goes by the sizes of the two, also where they cancel)
+    parts = lse.abs() + torch.where(live, safe.amax(1).abs(), torch.zeros((), dtype=torch.float64)) + math.log(e)
+    size = gb.abs() / n * p * (f + (p @ f)[:, None]) + gz.abs() / n * 2 * parts[:, None] * p
     if w is not None:
         wd, dwd = w.double(), grad_w.double()
         gate = wd * (dwd - (wd * dwd).sum(1, keepdim=True)) * live[:, None]
