@@ -657,12 +657,14 @@ hipError_t launch_tile(const Fp8Gemm& g, hipStream_t st) {
 // takes about 1.7 times as long in all. Small tiles win while they fit one
 // round: each has a CU to itself, and its stages wait on memory and on each
 // other, not on the matrix unit. N = 4096, K = 8192, us:
-//   rows   32x64 one  64x64 one  64x128 one  32x64  64x128  128x128  128x256  256x256
-//    128       15        18          23        22      28       35       53       71
-//    256       29        20          24        30      29       36       53       88
-//    512       53        36          27        50      31       37       54       88
-//   2048        -         -           -       204     119       82       71       99
-//   4096        -         -           -         -       -        -      155      117
+//   rows   32x32 one  32x64 one  64x64 one  64x128 one  32x64  64x128  128x128  128x256  256x256
+//     64       11        15         18          23        22      28       29       38       71
+//    128        -        15         18          23        22      28       35       53       71
+//    256        -        29         20          24        30      29       36       53       88
+//    512        -        53         36          27        50      31       37       54       88
+//   2048        -         -          -           -       204     119       82       71       99
+//   4096        -         -          -           -         -       -        -      155      117
+// (48 x 32: 33 rows of N = 8192, K = 4096 10.2 us against 11.0 with 32 x 64.)
 // 144 x 256 stands for experts of about 128 rows, half of which would take a
 // second, nearly empty tile of 128 (4096 tokens' down projection 1115 -> 1053 us;
 // experts of 109 rows 1014 against 1011).
@@ -670,17 +672,19 @@ struct TileShape {
   int rows, cols, first_ns, more_ns;
   bool one;
 };
-constexpr TileShape kTiles[] = {{32, 64, 230, 0, true},       {64, 64, 300, 0, true},       {64, 128, 420, 0, true},
-                                {32, 64, 340, 210, false},    {64, 128, 450, 450, false},   {128, 128, 620, 620, false},
-                                {128, 256, 1100, 1100, false}, {144, 256, 1200, 1200, false}, {256, 256, 1800, 1800, false}};
-constexpr int kNTiles = 9;
+enum { T32x32, T48x32, T32x64, T64x64, T64x128, T32x64Rounds, T64x128Rounds, T128x128, T128x256, T144x256, T256x256, kNTiles };
+constexpr TileShape kTiles[kNTiles] = {
+    {32, 32, 175, 0, true},        {48, 32, 195, 0, true},        {32, 64, 230, 0, true},
+    {64, 64, 300, 0, true},        {64, 128, 420, 0, true},       {32, 64, 340, 210, false},
+    {64, 128, 450, 450, false},    {128, 128, 620, 620, false},   {128, 256, 1100, 1100, false},
+    {144, 256, 1200, 1200, false}, {256, 256, 1800, 1800, false}};
 
 int best_tile(const Fp8Gemm& g) {
   // rows of one group: experts get theirs unevenly, by about the root of the mean
   const double mean = static_cast<double>(g.rows) / g.experts;
   const double rows = g.experts > 1 ? mean + std::sqrt(mean) : mean;
   const int groups = std::min(g.rows, g.experts);
-  int best = 3;
+  int best = T32x64Rounds;
   double least = 1e30;
   for (int i = 0; i < kNTiles; ++i) {
     const TileShape& t = kTiles[i];
@@ -704,26 +708,29 @@ int best_tile(const Fp8Gemm& g) {
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t st) {
   const int groups = std::min(g.rows, g.experts);
   const int mean = (g.rows - 1) / g.experts + 1;
-  // Few rows and little to stream: the streaming kernel (one pooler token 9 us
-  // against 13 with tiles, 16 tokens 12.3 against 13.3; 8 tokens on 4 experts
-  // 12.8 against 12.0 .. 13.0). Where the tiles fill the chip they read faster,
-  // whole 128-byte lines at a time (32 tokens' down projection 480 us against
-  // 510), and dense from 8192 weight rows on (N = 8192, K = 4096: 4 rows 9.3
-  // against 9.8, 16 rows 9.5 against 12.6).
-  if (g.rows <= 64 && mean <= 16 && static_cast<int64_t>(groups) * ((g.N + 63) / 64) < 2048 &&
-      !(g.experts == 1 && g.N >= 8192 && g.rows > 4))
+  // Few rows and little to stream: the streaming kernel (N = 4096, K = 8192: one
+  // row 9 us against 11 with tiles, 8 rows 10.4 against 10.9; 8 tokens on 4
+  // experts 12.8 against 12.0 .. 13.0). Where the tiles fill the chip they read
+  // faster, whole 128-byte lines at a time (32 tokens' down projection 480 us
+  // against 510), and dense over many weight rows (N = 8192, K = 4096: 4 rows 9.3
+  // against 9.8, 16 rows 9.5 against 12.6) or a long K (N = 4096, K = 8192: 16
+  // rows 10.9 against 12.3).
+  const bool tiles = g.experts == 1 && ((g.N >= 8192 && g.rows > 4) || (g.K >= 8192 && g.rows > 8));
+  if (g.rows <= 64 && mean <= 16 && static_cast<int64_t>(groups) * ((g.N + 63) / 64) < 2048 && !tiles)
     return launch_stream(g, groups, st);
   switch (best_tile(g)) {
+    case T32x32: return launch_tile<1, 2, 2, 1, 3, 4>(g, st);
+    case T48x32: return launch_tile<1, 2, 3, 1, 3, 4>(g, st);
     // (four blocks per stage where their decoding is the longer part: 33 rows in
     // fp32, N = 8192, K = 4096, 12.4 us against 13.6; bf16 11.0 against 10.5)
-    case 0: return g.f32 ? launch_tile_as<1, 4, 2, 1, 3, 4, true>(g, st) : launch_tile_as<1, 4, 2, 1, 4, 2, false>(g, st);
-    case 1: return launch_tile<2, 2, 2, 2, 3, 2>(g, st);
-    case 2: return launch_tile<2, 4, 2, 2, 3, 2>(g, st);
-    case 3: return launch_tile<1, 4, 2, 1, 4, 1>(g, st);
-    case 4: return launch_tile<2, 4, 2, 2, 4, 1>(g, st);
-    case 5: return launch_tile<2, 4, 4, 2, 4, 1>(g, st);
-    case 6: return launch_tile<2, 4, 4, 4, 3, 1>(g, st);
-    case 7: return launch_tile<1, 8, 9, 2, 3, 1>(g, st);
+    case T32x64: return g.f32 ? launch_tile_as<1, 4, 2, 1, 3, 4, true>(g, st) : launch_tile_as<1, 4, 2, 1, 4, 2, false>(g, st);
+    case T64x64: return launch_tile<2, 2, 2, 2, 3, 2>(g, st);
+    case T64x128: return launch_tile<2, 4, 2, 2, 3, 2>(g, st);
+    case T32x64Rounds: return launch_tile<1, 4, 2, 1, 4, 1>(g, st);
+    case T64x128Rounds: return launch_tile<2, 4, 2, 2, 4, 1>(g, st);
+    case T128x128: return launch_tile<2, 4, 4, 2, 4, 1>(g, st);
+    case T128x256: return launch_tile<2, 4, 4, 4, 3, 1>(g, st);
+    case T144x256: return launch_tile<1, 8, 9, 2, 3, 1>(g, st);
     // (wavefronts of 64 rows x 128 weight rows: 117 us for 4096 rows against 124
     // with 128 x 64, half the row scales to read and multiply)
     default: return launch_tile_as<4, 2, 4, 8, 2, 1, false>(g, st);

@@ -161,7 +161,7 @@ def test_linear(rows, n, k, dtype):
 
 
 # (rows, n, k) that fill the chip with each tile size, with ragged rows, weight rows and blocks of K
-WIDE = [(30, 9000, 400), (70, 8200, 1040), (200, 4000, 1040), (200, 4100, 400), (5, 20000, 528), (9, 65536, 144), (300, 5000, 272), (500, 4200, 1168), (520, 8200, 144),
+WIDE = [(30, 9000, 400), (33, 8000, 528), (48, 6001, 1040), (60, 8000, 400), (70, 8200, 1040), (200, 4000, 1040), (200, 4100, 400), (5, 20000, 528), (9, 65536, 144), (300, 5000, 272), (500, 4200, 1168), (520, 8200, 144),
         (1030, 8200, 144), (2100, 4200, 528), (2300, 8200, 256), (511, 20001, 144)]
 
 
