@@ -405,7 +405,8 @@ def fp8_grouped(x: torch.Tensor, x_scales: torch.Tensor, offsets: torch.Tensor, 
     """moe_fp8_grouped: rows offsets[e] .. offsets[e+1]-1 times expert e's
     weights, w [E][N][K] with w_scales [E][ceil(N/128)][ceil(K/128)], offsets
     [E+1] int32. The rows are those of x, or with row_index [rows] int32 row
-    row_index[i] // index_div of x for output row i."""
+    row_index[i] // index_div of x for output row i. Rows of out that no expert
+    takes are left as they are (as allocated, without out)."""
     _need(x.dim() == 2 and w.dim() == 3, "x: needs two dimensions, w three")
     dev = _device(x)
     (x_rows, K), (E, N, _) = x.shape, w.shape
