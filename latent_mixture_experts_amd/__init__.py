@@ -3,7 +3,7 @@
 The compute path is the C-ABI library ``libmoe.so`` (hand-written HIP kernels
 for gfx950), declared in ``include/moe.h``. This package holds:
 
-* :mod:`.binding` -- argument marshalling from torch tensors to the C-ABI;
+* :mod:`.binding` -- argument marshalling from torch tensors to the C-ABI
   (the layer's calls, and beside them the 8-bit rows and products and the
   router's balance loss);
 * :mod:`.build`   -- the hipcc build of ``libmoe.so``;
