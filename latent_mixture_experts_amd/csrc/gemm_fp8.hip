@@ -142,30 +142,33 @@ __device__ __forceinline__ int source_row(const Fp8Gemm& p, int r) {
   return min(max(v, 0), p.x_rows - 1);
 }
 
-// Four neighbouring outputs n .. n+3 of one row.
+// Four neighbouring outputs as they are stored (bf16: to nearest even, by the
+// conversion instruction).
 template <bool F32>
-__device__ __forceinline__ void store4(const Fp8Gemm& p, int row, int n, f32x4 v) {
-  const size_t at = static_cast<size_t>(row) * p.ldo + n;
-  if constexpr (F32) {
-    float* o = static_cast<float*>(p.out) + at;
-    if (p.out_vec && n + 4 <= p.N) {
-      *reinterpret_cast<f32x4*>(o) = v;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < p.N) o[i] = v[i];
-    }
+struct Out4 {
+  typedef float type;
+  f32x4 v;
+  __device__ __forceinline__ explicit Out4(f32x4 a) : v(a) {}
+};
+template <>
+struct Out4<false> {
+  typedef __bf16 type;
+  __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 v;
+  __device__ __forceinline__ explicit Out4(f32x4 a)
+      : v{static_cast<__bf16>(a[0]), static_cast<__bf16>(a[1]), static_cast<__bf16>(a[2]), static_cast<__bf16>(a[3])} {}
+};
+
+// Outputs n .. n+3 of one row, those that exist.
+template <bool F32>
+__device__ __forceinline__ void store4(const Fp8Gemm& p, int row, int n, f32x4 a) {
+  const Out4<F32> x(a);
+  auto* o = static_cast<typename Out4<F32>::type*>(p.out) + static_cast<size_t>(row) * p.ldo + n;
+  if (p.out_vec && n + 4 <= p.N) {
+    *reinterpret_cast<decltype(x.v)*>(o) = x.v;
   } else {
-    uint16_t* o = static_cast<uint16_t*>(p.out) + at;
-    if (p.out_vec && n + 4 <= p.N) {
-      *reinterpret_cast<uint2*>(o) =
-          uint2{f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16),
-                f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16)};
-    } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < p.N) o[i] = f32_to_bf16(v[i]);
-    }
+    for (int i = 0; i < 4; ++i)
+      if (n + i < p.N) o[i] = x.v[i];
   }
 }
 
@@ -590,14 +593,29 @@ __global__ __launch_bounds__(64 * WT * WW * KG) void fp8_tile_kernel(Fp8Gemm p, 
 #pragma unroll
         for (int f = 0; f < FW; ++f) acc[t][f] += part[((wave + (v - 1) * kGroup) * FT * FW + t * FW + f) * 64 + lane];
   }
+  const int n1 = n0 + ww * (FW * 16) + 4 * g;
+  if (p.out_vec && n0 + BN <= p.N) {  // (no part of the tile lies past the last weight row)
 #pragma unroll
-  for (int t = 0; t < FT; ++t) {
-    const int r = (t * WT + wt) * 16 + nl;
-    if (r >= nrows) continue;
+    for (int t = 0; t < FT; ++t) {
+      const int r = (t * WT + wt) * 16 + nl;
+      auto* o = static_cast<typename Out4<F32>::type*>(p.out) + static_cast<size_t>(grp.begin + r) * p.ldo + n1;
+      if (r < nrows) {
 #pragma unroll
-    for (int f = 0; f < FW; ++f) {
-      const int n = n0 + (ww * FW + f) * 16 + 4 * g;
-      if (n < p.N) store4<F32>(p, grp.begin + r, n, acc[t][f]);
+        for (int f = 0; f < FW; ++f) {
+          const Out4<F32> x(acc[t][f]);
+          *reinterpret_cast<decltype(x.v)*>(o + f * 16) = x.v;
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < FT; ++t) {
+      const int r = (t * WT + wt) * 16 + nl;
+      if (r < nrows) {
+#pragma unroll
+        for (int f = 0; f < FW; ++f)
+          if (n1 + f * 16 < p.N) store4<F32>(p, grp.begin + r, n1 + f * 16, acc[t][f]);
+      }
     }
   }
 }
