@@ -158,9 +158,23 @@ hipError_t launch_quant(const Fp8Quant& q, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_fp8_quant(const Fp8Quant& q, hipStream_t st) {
-  if (q.swiglu) return q.f32 ? launch_quant<true, true>(q, st) : launch_quant<false, true>(q, st);
-  return q.f32 ? launch_quant<true, false>(q, st) : launch_quant<false, false>(q, st);
+// A launch holds fewer than 2^32 threads, 16 per group: more than 2^24 rows take
+// several.
+hipError_t launch_fp8_quant(const Fp8Quant& all, hipStream_t st) {
+  constexpr int kRows = 1 << 24;
+  hipError_t e = hipSuccess;
+  for (int64_t r = 0; r < all.rows && e == hipSuccess; r += kRows) {
+    Fp8Quant q = all;
+    q.x = static_cast<const uint8_t*>(all.x) + r * all.ldx * (all.f32 ? 4 : 2);
+    q.codes += r * all.cols;
+    q.scales += r * fp8_blocks(all.cols);
+    q.rows = static_cast<int>(all.rows - r < kRows ? all.rows - r : kRows);
+    if (q.swiglu)
+      e = q.f32 ? launch_quant<true, true>(q, st) : launch_quant<false, true>(q, st);
+    else
+      e = q.f32 ? launch_quant<true, false>(q, st) : launch_quant<false, false>(q, st);
+  }
+  return e;
 }
 
 }  // namespace moe

@@ -241,3 +241,24 @@ def test_refusals():
     with pytest.raises(B.MoeError) as e:
         B.balance_loss(logits, ids, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == B.MOE_EWORKSPACE
+
+
+def test_offsets_past_32_bits():
+    """Rows of logits and gradients beyond 2^32 bytes: the same values as near
+    the start."""
+    few, E, K = 1024, 144, 4
+    logits, ids, w, dw, _ = case(few, E, K, False)
+    times = (1 << 32) // (4 * E * few) + 2
+    T = few * times
+    big = [t.cuda().repeat(times, 1) for t in (logits, ids, w, dw)]
+    losses, counts = B.balance_loss(big[0], big[1])
+    one, one_c = B.balance_loss(logits.cuda(), ids.cuda())
+    assert torch.equal(counts, one_c * times) and T * E * 4 > 1 << 32
+    # the same mean: sums of up to T / (64 * 256) + 16 + 256 positive terms, each addition half a step
+    tol = (T / (64 * 256) + 16 + 256) * R.U24
+    assert bool(((losses - one).abs() <= 2 * tol * one).all()), (losses, one)
+    gl = torch.tensor([0.7, 0.02], device="cuda") * T
+    got = B.balance_loss_backward(big[0], big[1], counts, gl, None, big[2], big[3]).view(times, few, E)
+    assert bool((got == got[0]).all())
+    ref, size = R.balance(logits, ids, None, gl.cpu() / times, w, dw)[2:]
+    check_grad(got[-1], ref, size)

@@ -473,3 +473,45 @@ def test_layer_in_eight_bits(tokens):
     ref = ref @ wd(*unpool).t()
     rel = float((out.double() - ref).norm() / ref.norm())
     assert rel < 4 * 2 * 2.0 ** -4 / 3 ** 0.5, rel
+
+
+# ---- offsets past 32 bits --------------------------------------------------
+
+MANY = (1 << 24) + 37  # rows: more than one launch of the quantisation takes
+
+
+def far_rows():
+    """Where offsets and launches turn over, and the ends."""
+    at = [0, MANY - 64, (1 << 24) - 32, (1 << 31) // 144 - 32, (1 << 32) // 288 - 32, (1 << 31) // 272 - 32]
+    return torch.cat([torch.arange(a, a + 64) for a in at])
+
+
+def test_quantize_of_many_rows():
+    x = torch.empty((MANY, 144), dtype=torch.bfloat16, device="cuda")
+    x.copy_(torch.arange(MANY, device="cuda")[:, None] % 1009 - 504)
+    x[:, 5:20] += torch.arange(15, device="cuda", dtype=torch.bfloat16)
+    codes, scales = B.fp8_quantize(x)
+    at = far_rows()
+    ref, ref_s = R.quantize_f32(x[at.cuda()].float().cpu())
+    assert torch.equal(scales[at.cuda()].cpu(), ref_s)
+    assert torch.equal(R.canonical(codes.view(torch.uint8)[at.cuda()].cpu()), ref)
+    # every row against the first of the same values
+    codes = codes.view(torch.uint8)
+    for r in range(0, MANY, 1009 << 10):
+        n = min(1009 << 10, MANY - r)
+        assert torch.equal(codes[r:r + n], codes[:n]) and torch.equal(scales[r:r + n], scales[:n]), r
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_linear_of_many_rows(dtype):
+    g = gen(3)
+    few, few_s, w, ws = operands(1009, 144, 144, g)
+    times = MANY // 1009 + 1
+    x = few.view(torch.uint8).cuda().repeat(times, 1)[:MANY].view(F8)
+    xs = few_s.cuda().repeat(times, 1)[:MANY].contiguous()
+    got = B.fp8_linear(x, xs, *dev(w, ws), dtype)
+    at = far_rows()
+    R.assert_product(got[at.cuda()].cpu(), x.view(torch.uint8)[at.cuda()].cpu().view(F8), xs[at.cuda()].cpu(), w, ws)
+    for r in range(0, MANY, 1009 << 10):  # (a row's sum does not depend on its place)
+        n = min(1009 << 10, MANY - r)
+        assert torch.equal(got[r:r + n], got[:n]), r
