@@ -298,6 +298,13 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
+def _int32(*sizes: int) -> None:
+    """(ctypes would cut a larger one off without a word)"""
+    for n in sizes:
+        if not -(1 << 31) <= n < 1 << 31:
+            raise ValueError(f"sizes are 32-bit, got {n}")
+
+
 def _check(name: str, t: torch.Tensor, dev: torch.device, types, shape, pitched: bool = False) -> None:
     """t is on dev, of one of the types, of that shape, and dense (pitched: its rows are, at any pitch)."""
     if (t.shape != shape or t.dtype not in types or t.device != dev or
@@ -314,6 +321,8 @@ def _pitch(t: torch.Tensor) -> int:
 
 def _run(what: str, dev: torch.device, stream, *args) -> None:
     fn = getattr(_lib or lib(), what)
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"the tensors are on {dev}, the stream on {stream.device}")
     # (the current stream's handle alone: building a torch.cuda.Stream costs as much as the launch)
     st = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
     if dev.index == torch._C._cuda_getDevice():
@@ -344,6 +353,7 @@ def _device(t: torch.Tensor) -> torch.device:
 def _quantize(what: str, x: torch.Tensor, cols: int, codes, scales, stream):
     dev = _device(x)
     rows = x.shape[0]
+    _int32(rows, cols)
     _check("x", x, dev, _ANY_FLOAT, (rows, x.shape[1]), pitched=True)
     if codes is None:
         codes = _empty((rows, cols), torch.float8_e4m3fn, dev, stream)
@@ -389,6 +399,7 @@ def fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     _need(x.dim() == 2 and w.dim() == 2, "x, w: need two dimensions")
     dev = _device(x)
     (T, K), N = x.shape, w.shape[0]
+    _int32(T, K, N)
     _check("x", x, dev, _CODES, (T, K), pitched=True)
     _check("x_scales", x_scales, dev, _F32, (T, _blocks(K)))
     _check("w", w, dev, _CODES, (N, K))
@@ -410,14 +421,14 @@ def fp8_grouped(x: torch.Tensor, x_scales: torch.Tensor, offsets: torch.Tensor, 
     _need(x.dim() == 2 and w.dim() == 3, "x: needs two dimensions, w three")
     dev = _device(x)
     (x_rows, K), (E, N, _) = x.shape, w.shape
-    rows = x_rows
+    rows = x_rows if row_index is None else row_index.numel()
+    _int32(rows, x_rows, K, E, N, index_div)
     _check("x", x, dev, _CODES, (x_rows, K), pitched=True)
     _check("x_scales", x_scales, dev, _F32, (x_rows, _blocks(K)))
     _check("offsets", offsets, dev, _I32, (E + 1,))
     _check("w", w, dev, _CODES, (E, N, K))
     _check("w_scales", w_scales, dev, _F32, (E, _blocks(N), _blocks(K)))
     if row_index is not None:
-        rows = row_index.numel()
         _check("row_index", row_index, dev, _I32, (rows,))
     out = _out(out, rows, N, out_dtype, dev, stream)
     _run("moe_fp8_grouped", dev, stream, rows, E, N, K, offsets.data_ptr(), _ptr(row_index), index_div,
@@ -427,6 +438,7 @@ def fp8_grouped(x: torch.Tensor, x_scales: torch.Tensor, offsets: torch.Tensor, 
 
 
 def balance_workspace_bytes(T: int, n_experts: int) -> int:
+    _int32(T, n_experts)
     return int(lib().moe_balance_workspace_bytes(T, n_experts))
 
 
@@ -438,6 +450,7 @@ def balance_loss(logits: torch.Tensor, ids: torch.Tensor, mask=None, ws=None, st
     _need(logits.dim() == 2 and ids.dim() == 2, "logits, ids: need two dimensions")
     dev = _device(logits)
     (T, E), K = logits.shape, ids.shape[1]
+    _int32(T, E, K)
     _check("logits", logits, dev, _F32, (T, E))
     _check("ids", ids, dev, _I32, (T, K))
     if mask is not None:
@@ -464,6 +477,7 @@ def balance_loss_backward(logits: torch.Tensor, ids: torch.Tensor, counts: torch
     _need(logits.dim() == 2 and ids.dim() == 2, "logits, ids: need two dimensions")
     dev = _device(logits)
     (T, E), K = logits.shape, ids.shape[1]
+    _int32(T, E, K)
     _check("logits", logits, dev, _F32, (T, E))
     _check("ids", ids, dev, _I32, (T, K))
     _check("counts", counts, dev, _I32, (E + 1,))

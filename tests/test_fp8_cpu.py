@@ -2,6 +2,8 @@
 argument checks, and the oracle against definitions of its own."""
 from __future__ import annotations
 
+import types
+
 import pytest
 import torch
 
@@ -143,6 +145,21 @@ def test_host_tensors_are_refused():
         B.fp8_quantize(x)
     with pytest.raises(ValueError):
         B.balance_loss(torch.zeros((4, 8)), torch.zeros((4, 2), dtype=torch.int32))
+
+
+def test_a_stream_of_another_device_is_refused():
+    stream = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    with pytest.raises(ValueError, match="stream"):
+        B._run("moe_fp8_quantize", torch.device("cuda", 0), stream)
+
+
+def test_sizes_past_32_bits():
+    B._int32(0, -1, 2 ** 31 - 1)
+    for n in (2 ** 31, 2 ** 32 + 1, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match="32-bit"):
+            B._int32(1, n)
+    with pytest.raises(ValueError, match="32-bit"):
+        B.balance_workspace_bytes(2 ** 32 + 4096, 16)
 
 
 def test_oracle_rounds_to_e4m3():

@@ -515,3 +515,15 @@ def test_linear_of_many_rows(dtype):
     for r in range(0, MANY, 1009 << 10):  # (a row's sum does not depend on its place)
         n = min(1009 << 10, MANY - r)
         assert torch.equal(got[r:r + n], got[:n]), r
+
+
+def test_sizes_past_32_bits_are_refused():
+    x = torch.empty((1 << 31, 16), dtype=torch.uint8, device="cuda")
+    xs = torch.empty((1 << 31, 1), device="cuda")
+    w, ws = torch.zeros((16, 16), dtype=torch.uint8, device="cuda"), torch.ones((1, 1), device="cuda")
+    with pytest.raises(ValueError, match="32-bit"):
+        B.fp8_linear(x, xs, w, ws)
+    off = torch.zeros(2, dtype=torch.int32, device="cuda")
+    index = torch.zeros(4, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="32-bit"):
+        B.fp8_grouped(x[:4], xs[:4], off, w[None], ws[None], row_index=index, index_div=(1 << 32) + 1)
