@@ -37,16 +37,18 @@ __device__ __forceinline__ uint32_t row16_max_u32(uint32_t v) {
 
 // silu(g) = g / (1 + exp(-g)) through the exponential and reciprocal
 // instructions (1 ulp each): the exponent's rounding error, up to |g| * 2^-24
-// of the result, is taken back by its low part. Beyond +-200 the exponential
-// is 0 or infinite anyway; the bound keeps the low part finite, and below -88,
-// where the exponential may be infinite, it is left out (inf - inf).
+// of the result, is taken back by its low part. The exponent stops just below
+// 128; what a gate asks beyond that is in the low part too, and an exponential
+// past fp32 comes out infinite, the result zero. The reciprocal instruction
+// gives zero for what lies past 2^126 (gates below -87.3), so it takes an eighth
+// of the sum: its result times 1/8 is exact, or a denormal off by 2^-22 at most.
 __device__ __forceinline__ float silu(float g) {
   constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.693147182f;
-  const float b = __builtin_amdgcn_fmed3f(g, -200.0f, 200.0f);
-  const float t = b * kLog2e;
-  const float low = fmaf(b, kLog2eLow, fmaf(b, kLog2e, -t));
-  const float e = __builtin_amdgcn_exp2f(-t);
-  return g * __builtin_amdgcn_rcpf(1.0f + (b > -88.0f ? fmaf(e * kLn2, -low, e) : e));
+  const float b = __builtin_amdgcn_fmed3f(g, -1e30f, 200.0f);
+  const float t = fminf(-b * kLog2e, 0x1.fffffep+6f);
+  const float low = fmaf(-b, kLog2eLow, fmaf(-b, kLog2e, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return g * (__builtin_amdgcn_rcpf(fmaf(fmaf(e * kLn2, low, e), 0.125f, 0.125f)) * 0.125f);
 }
 
 // Eight consecutive values.

@@ -109,6 +109,23 @@ def test_swiglu_of_far_gates():
     assert float(back.abs().max()) < 2.0 ** -90
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_swiglu_of_gates_up_to_the_exponentials_overflow(dtype):
+    """exp(-gate) between 2^126 and fp32's largest value: silu is a normal
+    number there, and a large up value makes it count."""
+    gate = torch.cat([torch.linspace(-88.7228, -86.0, 500), torch.linspace(-88.5, -40.0, 98),
+                      torch.tensor([-88.5, -88.0])]).to(dtype)
+    gate = gate[gate > -88.7229]  # (as the type rounds it)
+    gu = torch.cat([gate[:, None].expand(-1, 128), torch.full((gate.numel(), 128), 2.0 ** 100)], 1).to(dtype)
+    codes, scales = B.fp8_swiglu(gu.cuda())
+    d = gu[:, 0].double()
+    h = d * torch.sigmoid(d) * 2.0 ** 100
+    # exponential and reciprocal two half steps each, five roundings, one of a denormal above 2^-128: 4; under
+    # 16 half steps; the scale's quotient one more. Every value of a group is its largest: code -448.
+    assert bool(((scales[:, 0].cpu().double() * 448 / -h - 1).abs() <= 18 * R.U24).all())
+    assert bool((codes.float() == -448).all())
+
+
 def test_swiglu_non_finite():
     gu = torch.ones((4, 256))
     gu[0, 3] = float("nan")
