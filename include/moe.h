@@ -385,10 +385,16 @@ int moe_fp8_swiglu(int32_t rows, int32_t inter, const void *gate_up, int64_t ld,
  *   x [T][K] codes (pitch ldx), x_scales [T][ceil(K/128)],
  *   w [N][K] codes, w_scales [ceil(N/128)][ceil(K/128)],
  *   out [T][N] (pitch ldo) of out_type, rounded once from an fp32 sum of the
- *   blocks. Within a block an fp32 out sums in fp32; a bf16 out may drop what
- *   lies 2^-14 below the largest of eight neighbouring products (the E4M3
- *   matrix instruction's own sum): inside its final rounding unless the terms
- *   cancel each other. */
+ *   blocks. Within a block an fp32 out sums in fp32. A bf16 out does so for few
+ *   rows; otherwise it takes the E4M3 matrix instruction's own sum, which drops
+ *   from each eight neighbouring products what lies 2^-14 below the largest of
+ *   them, up to 7 * 2^-14 of it: inside its final rounding unless the terms
+ *   cancel each other, when it may be off in all its bits. Which of the two goes
+ *   by the sizes (rows, N, K, experts), so the rows beside a row can change its
+ *   result by that much. With MOE_SUM_F32 added to out_type a bf16 out sums in
+ *   fp32 always, at 1.1 times the time for tens of rows and up to 2.1 times for
+ *   thousands; what is left to the sizes then is the order of fp32 additions. */
+#define MOE_SUM_F32 0x100
 int moe_fp8_linear(int32_t T, int32_t N, int32_t K, const uint8_t *x,
                    int64_t ldx, const float *x_scales, const uint8_t *w,
                    const float *w_scales, void *out, int64_t ldo,

@@ -283,6 +283,7 @@ def workspace_view(d: MoeDims, T: int, ws: torch.Tensor, which: str, dtype, shap
 # run on the tensors' device, on its current stream unless one is given (a
 # torch.cuda.Stream; what they allocate then belongs to that stream).
 TYPE_BF16, TYPE_F32 = 0, 1  # MOE_TYPE_*
+SUM_F32 = 0x100  # MOE_SUM_F32
 _FLOATS = {torch.bfloat16: TYPE_BF16, torch.int16: TYPE_BF16, torch.float32: TYPE_F32}  # int16: bf16 bits
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 _ANY_FLOAT = tuple(_FLOATS)
@@ -393,10 +394,11 @@ def _out(out, rows: int, n: int, dtype, dev: torch.device, stream) -> torch.Tens
 
 
 def fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
-               out_dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+               out_dtype=torch.bfloat16, out=None, stream=None, f32_sums: bool = False) -> torch.Tensor:
     """moe_fp8_linear: x [T][K] e4m3 with x_scales [T][ceil(K/128)], times w
     [N][K] e4m3 with w_scales [ceil(N/128)][ceil(K/128)] -> [T][N] of
-    out_dtype, or into out. Rows of x and out at any pitch."""
+    out_dtype, or into out. Rows of x and out at any pitch. f32_sums: a bf16
+    out, too, sums in fp32 throughout (MOE_SUM_F32)."""
     _need(x.dim() == 2 and w.dim() == 2, "x, w: need two dimensions")
     dev = _device(x)
     (T, K), N = x.shape, w.shape[0]
@@ -407,18 +409,20 @@ def fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     _check("w_scales", w_scales, dev, _F32, (_blocks(N), _blocks(K)))
     out = _out(out, T, N, out_dtype, dev, stream)
     _run("moe_fp8_linear", dev, stream, T, N, K, x.data_ptr(), _pitch(x), x_scales.data_ptr(),
-         w.data_ptr(), w_scales.data_ptr(), out.data_ptr(), _pitch(out), _FLOATS[out.dtype])
+         w.data_ptr(), w_scales.data_ptr(), out.data_ptr(), _pitch(out),
+         _FLOATS[out.dtype] | SUM_F32 if f32_sums else _FLOATS[out.dtype])
     return out
 
 
 def fp8_grouped(x: torch.Tensor, x_scales: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
                 w_scales: torch.Tensor, out_dtype=torch.bfloat16, row_index=None, index_div: int = 1,
-                out=None, stream=None) -> torch.Tensor:
+                out=None, stream=None, f32_sums: bool = False) -> torch.Tensor:
     """moe_fp8_grouped: rows offsets[e] .. offsets[e+1]-1 times expert e's
     weights, w [E][N][K] with w_scales [E][ceil(N/128)][ceil(K/128)], offsets
     [E+1] int32. The rows are those of x, or with row_index [rows] int32 row
     row_index[i] // index_div of x for output row i. Rows of out that no expert
-    takes are left as they are (as allocated, without out)."""
+    takes are left as they are (as allocated, without out). f32_sums as for
+    fp8_linear."""
     _need(x.dim() == 2 and w.dim() == 3, "x: needs two dimensions, w three")
     dev = _device(x)
     (x_rows, K), (E, N, _) = x.shape, w.shape
@@ -434,7 +438,7 @@ def fp8_grouped(x: torch.Tensor, x_scales: torch.Tensor, offsets: torch.Tensor, 
     out = _out(out, rows, N, out_dtype, dev, stream)
     _run("moe_fp8_grouped", dev, stream, rows, E, N, K, offsets.data_ptr(), _ptr(row_index), index_div,
          x_rows, x.data_ptr(), _pitch(x), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
-         out.data_ptr(), _pitch(out), _FLOATS[out.dtype])
+         out.data_ptr(), _pitch(out), _FLOATS[out.dtype] | SUM_F32 if f32_sums else _FLOATS[out.dtype])
     return out
 
 

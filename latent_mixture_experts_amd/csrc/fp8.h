@@ -40,6 +40,7 @@ struct Fp8Gemm {
   int64_t ldx, ldo;
   int rows, x_rows, experts, N, K, index_div;
   bool f32;       // out fp32, else bf16
+  bool exact;     // blocks are summed in fp32 (always when f32)
   bool out_vec;   // out rows take four-value stores (base and pitch aligned)
 };
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t st);

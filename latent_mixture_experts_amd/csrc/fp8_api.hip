@@ -24,6 +24,9 @@ int need(const void* p, size_t n) {
 
 int type_ok(int32_t type) { return type == MOE_TYPE_BF16 || type == MOE_TYPE_F32 ? MOE_OK : MOE_EINVAL; }
 
+// The type of a product's out without MOE_SUM_F32.
+int32_t out_type_of(int32_t type) { return type >= 0 ? type & ~MOE_SUM_F32 : type; }
+
 #define MOE_TRY(expr)              \
   do {                             \
     const int rc_ = (expr);        \
@@ -63,7 +66,7 @@ int run_quant(int32_t rows, int32_t cols, const void* x, int64_t ldx, int32_t ty
 int check_product(int32_t rows, int32_t N, int32_t K, const uint8_t* x, int64_t ldx, const float* xs,
                   const uint8_t* w, const float* ws, const void* out, int64_t ldo, int32_t type) {
   if (rows < 0 || N <= 0 || K <= 0) return MOE_EINVAL;
-  MOE_TRY(type_ok(type));
+  MOE_TRY(type_ok(out_type_of(type)));
   if (rows >= kMaxRows || K % 16 || K > kMaxWidth || N > kMaxWidth) return MOE_EUNSUPPORTED;
   if (ldx < K || ldo < N) return MOE_EINVAL;
   if (ldx > kMaxPitch || ldo > kMaxPitch) return MOE_EUNSUPPORTED;
@@ -72,7 +75,7 @@ int check_product(int32_t rows, int32_t N, int32_t K, const uint8_t* x, int64_t 
   MOE_TRY(need(xs, 4));
   MOE_TRY(need(w, 16));
   MOE_TRY(need(ws, 4));
-  MOE_TRY(need(out, type == MOE_TYPE_F32 ? 4 : 2));
+  MOE_TRY(need(out, out_type_of(type) == MOE_TYPE_F32 ? 4 : 2));
   if (ldx % 16) return MOE_EALIGN;
   return MOE_OK;
 }
@@ -92,7 +95,8 @@ moe::Fp8Gemm product(int32_t rows, int32_t N, int32_t K, const uint8_t* x, int64
   g.N = N;
   g.K = K;
   g.index_div = 1;
-  g.f32 = type == MOE_TYPE_F32;
+  g.f32 = out_type_of(type) == MOE_TYPE_F32;
+  g.exact = type != MOE_TYPE_BF16;
   g.out_vec = ldo % 4 == 0 && aligned(out, g.f32 ? 16 : 8);
   return g;
 }

@@ -13,11 +13,14 @@
 // Two ways to sum a block. The E4M3 MFMA 16x16x128 takes it in one
 // instruction at twice the bf16 rate, but adds each eight neighbouring products
 // on a grid 2^-14 of the largest of them and drops what lies below (measured; the
-// eights are then added in fp32; a block's sum came out up to 2^-11 of its largest
-// product off, 1.5e-5 of the sums' norm for normal operands): enough for outputs
-// rounded to bf16 (2^-9 each), not for fp32 ones. There, and wherever the
-// weights' way from HBM bounds the kernel anyway, the codes become bf16 (exact)
-// and four bf16 MFMAs 16x16x32 sum the block to fp32 (measured: 1e-8 of the norm).
+// eights are then added in fp32): each eight may come out 7 * 2^-14 of its
+// largest product off, a block up to 2^-7.2 of its largest. For normal operands a
+// sum is 1.5e-5 of the sums' norm off, which a bf16 rounding (half a step: up to
+// 2^-8 of the value) hides; where the terms cancel it may be all that is left. The
+// tiles with bf16 out take it, whatever bounds them, unless the caller asks for
+// fp32 sums (MOE_SUM_F32). Those, fp32 outs and the streaming kernel turn the
+// codes into bf16 (exact) and sum the block to fp32 by four bf16 MFMAs 16x16x32
+// (measured: 1e-8 of the norm).
 #include <algorithm>
 #include <cmath>
 
@@ -52,7 +55,7 @@ __device__ __forceinline__ bf16x8 e4m3x8_to_bf16(int lo, int hi) {
 
 // An operand fragment, 16 rows x one block, as the matrix instructions take it:
 // the codes, or (EXACT) their bf16 values, decoded once for all the products it
-// enters. Lane l holds 32 bytes of row l%16; which 32 of the block's 128 lane
+// enters, for sums in fp32. Lane l holds 32 bytes of row l%16; which 32 of the block's 128 lane
 // group l/16 holds is free as long as both operands agree, since the block is
 // summed whole.
 template <bool EXACT>
@@ -308,7 +311,7 @@ __device__ __forceinline__ uint32_t lds_address(const T* p) {
   return static_cast<uint32_t>(reinterpret_cast<size_t>((__attribute__((address_space(3))) T*)(p)));
 }
 
-template <int WT, int WW, int FT, int FW, int R, int KG, bool F32>
+template <int WT, int WW, int FT, int FW, int R, int KG, bool F32, bool EXACT>
 __global__ __launch_bounds__(64 * WT * WW * KG) void fp8_tile_kernel(Fp8Gemm p, int n_row_tiles, int n_col_tiles, int chunk) {
   constexpr int kGroup = WT * WW, NW = kGroup * KG, BM = WT * FT * 16, BN = WW * FW * 16;
   // 1-KiB copies per wavefront and stage (its group's block); of the rows' some
@@ -510,7 +513,7 @@ __global__ __launch_bounds__(64 * WT * WW * KG) void fp8_tile_kernel(Fp8Gemm p, 
         const int set = KG == 1 ? (st / kFSet) & 1 : slot, blk = KG == 1 ? st % kFSet : kg;
         return Sw[set][(n0 % kFp8Block + ww * (FW * 16)) / kFp8Block * kFSet + blk];
       };
-      Operand<F32> wv[FW], xv;
+      Operand<EXACT> wv[FW], xv;
 #pragma unroll
       for (int f = 0; f < FW; ++f) wv[f].set(read_w(0, f));
       i32x8 next = read_x(0, 0);
@@ -643,7 +646,7 @@ hipError_t launch_stream(const Fp8Gemm& g, int groups, hipStream_t st) {
   return launch_stream_ks<8, 2>(g, tiles, groups, st);
 }
 
-template <int WT, int WW, int FT, int FW, int R, int KG, bool F32>
+template <int WT, int WW, int FT, int FW, int R, int KG, bool F32, bool EXACT>
 hipError_t launch_tile_as(const Fp8Gemm& g, hipStream_t st) {
   constexpr int BM = WT * FT * 16, BN = WW * FW * 16;
   const int nct = (g.N + BN - 1) / BN;
@@ -660,19 +663,25 @@ hipError_t launch_tile_as(const Fp8Gemm& g, hipStream_t st) {
   } else {
     grid = (nrt * nct + 7) / 8 * 8;
   }
-  MOE_LAUNCH((fp8_tile_kernel<WT, WW, FT, FW, R, KG, F32>), dim3(grid), dim3(64 * WT * WW * KG), 0, st, g, nrt, nct, chunk);
+  MOE_LAUNCH((fp8_tile_kernel<WT, WW, FT, FW, R, KG, F32, EXACT>), dim3(grid), dim3(64 * WT * WW * KG), 0, st, g, nrt, nct, chunk);
   return hipGetLastError();
 }
 template <int WT, int WW, int FT, int FW, int R, int KG>
+hipError_t launch_tile_exact(const Fp8Gemm& g, hipStream_t st) {
+  return g.f32 ? launch_tile_as<WT, WW, FT, FW, R, KG, true, true>(g, st)
+               : launch_tile_as<WT, WW, FT, FW, R, KG, false, true>(g, st);
+}
+template <int WT, int WW, int FT, int FW, int R, int KG>
 hipError_t launch_tile(const Fp8Gemm& g, hipStream_t st) {
-  return g.f32 ? launch_tile_as<WT, WW, FT, FW, R, KG, true>(g, st) : launch_tile_as<WT, WW, FT, FW, R, KG, false>(g, st);
+  return g.exact ? launch_tile_exact<WT, WW, FT, FW, R, KG>(g, st)
+                 : launch_tile_as<WT, WW, FT, FW, R, KG, false, false>(g, st);
 }
 
 // The tiles: rows, weight rows, and what one block of K takes in ns: in the
 // first round of workgroups, and in each further one (the 32 x 64 ones share a CU
 // with others, so their further rounds overlap). `one`: for a single round
-// only, with stages of several blocks. Measured at K = 8192 in bf16 out; fp32 out
-// takes about 1.7 times as long in all. Small tiles win while they fit one
+// only, with stages of several blocks. Measured at K = 8192 in bf16 out; fp32 sums
+// take 1.2 times as long for 64 rows, 1.5 for 256, 1.7 for 2048, 2.1 for 4096. Small tiles win while they fit one
 // round: each has a CU to itself, and its stages wait on memory and on each
 // other, not on the matrix unit. N = 4096, K = 8192, us:
 //   rows   32x32 one  32x64 one  64x64 one  64x128 one  32x64  64x128  128x128  128x256  256x256
@@ -708,7 +717,7 @@ int best_tile(const Fp8Gemm& g) {
     const TileShape& t = kTiles[i];
     // 256 x 256: its sums fill the registers, no room for bf16 operands; and
     // partly filled ones waste most (experts of 128 rows: 1153 us against 1051)
-    if (t.rows == 256 && (g.f32 || (g.experts > 1 && mean < 512))) continue;
+    if (t.rows == 256 && (g.exact || (g.experts > 1 && mean < 512))) continue;
     const double tiles = groups * std::ceil(rows / t.rows) * std::ceil(static_cast<double>(g.N) / t.cols);
     if (t.one && tiles > 256.0) continue;
     const double rounds = t.more_ns == t.first_ns ? std::ceil(tiles / 256.0) : std::max(1.0, tiles / 256.0);
@@ -741,7 +750,7 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t st) {
     case T48x32: return launch_tile<1, 2, 3, 1, 3, 4>(g, st);
     // (four blocks per stage where their decoding is the longer part: 33 rows in
     // fp32, N = 8192, K = 4096, 12.4 us against 13.6; bf16 11.0 against 10.5)
-    case T32x64: return g.f32 ? launch_tile_as<1, 4, 2, 1, 3, 4, true>(g, st) : launch_tile_as<1, 4, 2, 1, 4, 2, false>(g, st);
+    case T32x64: return g.exact ? launch_tile_exact<1, 4, 2, 1, 3, 4>(g, st) : launch_tile_as<1, 4, 2, 1, 4, 2, false, false>(g, st);
     case T64x64: return launch_tile<2, 2, 2, 2, 3, 2>(g, st);
     case T64x128: return launch_tile<2, 4, 2, 2, 3, 2>(g, st);
     case T32x64Rounds: return launch_tile<1, 4, 2, 1, 4, 1>(g, st);
@@ -751,7 +760,7 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t st) {
     case T144x256: return launch_tile<1, 8, 9, 2, 3, 1>(g, st);
     // (wavefronts of 64 rows x 128 weight rows: 117 us for 4096 rows against 124
     // with 128 x 64, half the row scales to read and multiply)
-    default: return launch_tile_as<4, 2, 4, 8, 2, 1, false>(g, st);
+    default: return launch_tile_as<4, 2, 4, 8, 2, 1, false, false>(g, st);
   }
 }
 

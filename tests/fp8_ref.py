@@ -93,6 +93,26 @@ def random_scales(shape, gen):
     return torch.exp(torch.randn(shape, generator=gen)) * 0.01
 
 
+def cancelling(rows, n, k, gen, experts=None):
+    """Operands (codes, power-of-two scales) of whole numbers whose sums fp32
+    holds in any order, and sums of fewer bits do not: every block has one
+    product of 2^16 and one of -2^16, in different eights, beside products of
+    at most 4. A block's partial sums stay below 2^18, its sum below 2^9, all of
+    them quarters at least after the scales."""
+    lead = () if experts is None else (experts,)
+    x = torch.randint(-2, 3, (rows, k), generator=gen).float()
+    w = torch.randint(-2, 3, (*lead, n, k), generator=gen).float()
+    for b in range(0, k, 128):
+        two = torch.randperm(min(128, k - b) // 8, generator=gen)[:2] * 8 + b
+        at = two + torch.randint(0, 8, (2,), generator=gen)
+        x[:, at] = 256.0
+        sign = torch.randint(0, 2, (*lead, n), generator=gen) * 2 - 1
+        w[..., at[0]], w[..., at[1]] = 256.0 * sign, -256.0 * sign
+    scales = lambda *shape: torch.exp2(torch.randint(-1, 2, shape, generator=gen).float())
+    f8 = torch.float8_e4m3fn
+    return x.to(f8), scales(rows, blocks(k)), w.to(f8), scales(*lead, blocks(n), blocks(k))
+
+
 def balance(logits, ids, mask=None, grad_losses=None, w=None, grad_w=None, counts=None):
     """(losses [2], counts [E+1], grad) in fp64; counts given: the gradient takes those."""
     lg = logits.double()

@@ -81,6 +81,32 @@ def test_product_arguments(fn):
         assert fn(**big) == B.MOE_EUNSUPPORTED, big
 
 
+@pytest.mark.parametrize("fn", [_linear, _grouped])
+def test_product_sum_flag(fn):
+    assert fn(t=B.TYPE_BF16 | B.SUM_F32, out=P + 2) == B.MOE_OK
+    assert fn(t=B.TYPE_F32 | B.SUM_F32) == B.MOE_OK
+    assert fn(t=B.TYPE_F32 | B.SUM_F32, out=P + 2) == B.MOE_EALIGN
+    for bad in (2, 2 | B.SUM_F32, 2 * B.SUM_F32, -1, -B.SUM_F32, -2 ** 31):
+        assert fn(t=bad) == B.MOE_EINVAL, bad
+    assert _quant(t=B.TYPE_BF16 | B.SUM_F32) == B.MOE_EINVAL  # of products' outs alone
+
+
+def test_cancelling_operands_separate_the_sums():
+    """Exact in fp32 in whatever order; with the smaller terms of an eight
+    dropped (their matrix instruction's grid, 2^-14 of the largest), not."""
+    g = torch.Generator().manual_seed(1)
+    for k in (16, 144, 400, 8192):
+        x, xs, w, ws = R.cancelling(9, 11, k, g)
+        want = R.product(x, xs, w, ws)[0]
+        terms = x.float()[:, None, :] * w.float()[None, :, :] * R.expand(xs, k).float()[:, None, :]
+        terms = terms * R.expand(ws, k).float()[:1].expand(11, -1)
+        order = torch.randperm(k, generator=g)
+        assert torch.equal(terms[..., order].cumsum(-1)[..., -1].double(), want)
+        top = torch.nn.functional.pad(terms, (0, -k % 8)).view(9, 11, -1, 8).abs().amax(-1).repeat_interleave(8, -1)
+        kept = torch.where(terms.abs() >= top[..., :k] * 2.0 ** -14, terms, torch.zeros(()))
+        assert float((kept.sum(-1).double() != want).double().mean()) > 0.5
+
+
 def test_grouped_arguments():
     assert _grouped(E=0) == B.MOE_EINVAL
     assert _grouped(E=257) == B.MOE_EUNSUPPORTED

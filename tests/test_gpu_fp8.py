@@ -220,6 +220,41 @@ def test_grouped_few_rows_wide(n, k, dtype):
     check_grouped(got, x, xs, w, ws, bounds)
 
 
+@pytest.mark.parametrize("rows,n,k", SHAPES + WIDE)
+def test_sums_in_fp32_lose_nothing(rows, n, k):
+    """Sums that cancel to less than 2^-14 of their terms: exact with an fp32
+    out, and rounded once from the exact one in bf16 with f32_sums; the bf16
+    default within what it may drop."""
+    x, xs, w, ws = ops = dev(*R.cancelling(rows, n, k, gen(rows + n + k)))
+    want = R.product(*ops)[0]
+    assert torch.equal(B.fp8_linear(*ops, torch.float32).double(), want)
+    assert torch.equal(B.fp8_linear(*ops, f32_sums=True), want.float().bfloat16())
+    out = torch.empty((rows, n + 3), device="cuda")[:, 3:]
+    B.fp8_linear(*ops, out=out, f32_sums=True)
+    assert torch.equal(out.double(), want)
+    R.assert_product(B.fp8_linear(*ops), *ops)
+
+
+GROUPS = [(90, 1, 2100, 272), (256, 20, 300, 144), (30, 40, 2100, 400), (60, 40, 3000, 144), (30, 60, 4200, 144),
+          (30, 130, 2100, 272), (4, 600, 4200, 144), (8, 375, 700, 1040), (5, 2, 272, 640)]
+
+
+@pytest.mark.parametrize("experts,mean,n,k", GROUPS)
+def test_grouped_sums_in_fp32_lose_nothing(experts, mean, n, k):
+    g = gen(experts + mean + n)
+    sizes = torch.randint(0, 2 * mean + 1, (experts,), generator=g).tolist()
+    bounds = [0] + torch.tensor(sizes).cumsum(0).tolist()
+    x, xs, w, ws = dev(*R.cancelling(bounds[-1], n, k, g, experts))
+    off = torch.tensor(bounds, dtype=torch.int32).cuda()
+    wide = B.fp8_grouped(x, xs, off, w, ws, torch.float32)
+    half = B.fp8_grouped(x, xs, off, w, ws, f32_sums=True)
+    for e, (a, b) in enumerate(zip(bounds, bounds[1:])):
+        if b > a:
+            want = R.product(x[a:b], xs[a:b], w[e], ws[e])[0]
+            assert torch.equal(wide[a:b].double(), want) and torch.equal(half[a:b], want.float().bfloat16()), e
+    check_grouped(B.fp8_grouped(x, xs, off, w, ws), x, xs, w, ws, bounds)
+
+
 @pytest.mark.parametrize("rows", [1, 20, 40, 150])
 def test_every_position_counts_once(rows):
     """One nonzero code per row of x and every code value in w: out is that code times the scales."""
