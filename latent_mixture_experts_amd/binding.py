@@ -281,7 +281,9 @@ def workspace_view(d: MoeDims, T: int, ws: torch.Tensor, which: str, dtype, shap
 # These take their sizes from the tensors, so they check them: a wrong shape,
 # type, layout or device raises ValueError before anything is enqueued. They
 # run on the tensors' device, on its current stream unless one is given (a
-# torch.cuda.Stream; what they allocate then belongs to that stream).
+# torch.cuda.Stream). What they allocate then belongs to that stream, and what
+# they were given may be dropped once they return; order between the streams
+# (inputs written before, results read after, there or elsewhere) is the caller's.
 TYPE_BF16, TYPE_F32 = 0, 1  # MOE_TYPE_*
 SUM_F32 = 0x100  # MOE_SUM_F32
 _FLOATS = {torch.bfloat16: TYPE_BF16, torch.int16: TYPE_BF16, torch.float32: TYPE_F32}  # int16: bf16 bits
@@ -345,6 +347,15 @@ def _empty(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+def _hold(stream, *tensors) -> None:
+    """Memory of the call's tensors is not handed out again before the given
+    stream has done the call, also when the caller drops them right after it."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _device(t: torch.Tensor) -> torch.device:
     dev = t.device
     if dev.type != "cuda":
@@ -365,6 +376,7 @@ def _quantize(what: str, x: torch.Tensor, cols: int, codes, scales, stream):
         scales = _empty((rows, _blocks(cols)), torch.float32, dev, stream)
     else:
         _check("scales", scales, dev, _F32, (rows, _blocks(cols)))
+    _hold(stream, x, codes, scales)
     _run(what, dev, stream, rows, cols, x.data_ptr(), _pitch(x), _FLOATS[x.dtype], codes.data_ptr(),
          scales.data_ptr())
     return codes, scales
@@ -408,6 +420,7 @@ def fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     _check("w", w, dev, _CODES, (N, K))
     _check("w_scales", w_scales, dev, _F32, (_blocks(N), _blocks(K)))
     out = _out(out, T, N, out_dtype, dev, stream)
+    _hold(stream, x, x_scales, w, w_scales, out)
     _run("moe_fp8_linear", dev, stream, T, N, K, x.data_ptr(), _pitch(x), x_scales.data_ptr(),
          w.data_ptr(), w_scales.data_ptr(), out.data_ptr(), _pitch(out),
          _FLOATS[out.dtype] | SUM_F32 if f32_sums else _FLOATS[out.dtype])
@@ -436,6 +449,7 @@ def fp8_grouped(x: torch.Tensor, x_scales: torch.Tensor, offsets: torch.Tensor, 
     if row_index is not None:
         _check("row_index", row_index, dev, _I32, (rows,))
     out = _out(out, rows, N, out_dtype, dev, stream)
+    _hold(stream, x, x_scales, offsets, w, w_scales, row_index, out)
     _run("moe_fp8_grouped", dev, stream, rows, E, N, K, offsets.data_ptr(), _ptr(row_index), index_div,
          x_rows, x.data_ptr(), _pitch(x), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
          out.data_ptr(), _pitch(out), _FLOATS[out.dtype] | SUM_F32 if f32_sums else _FLOATS[out.dtype])
@@ -467,6 +481,7 @@ def balance_loss(logits: torch.Tensor, ids: torch.Tensor, mask=None, ws=None, st
         _check("ws", ws, dev, (torch.uint8,), (ws.numel(),))
     losses = _empty(2, torch.float32, dev, stream)
     counts = _empty(E + 1, torch.int32, dev, stream)
+    _hold(stream, logits, ids, mask, ws)
     _run("moe_balance_loss", dev, stream, T, E, K, logits.data_ptr(), ids.data_ptr(), _ptr(mask),
          counts.data_ptr(), losses.data_ptr(), _ptr(ws), ws.numel() if ws is not None else 0)
     return losses, counts
@@ -497,6 +512,7 @@ def balance_loss_backward(logits: torch.Tensor, ids: torch.Tensor, counts: torch
         out = _empty((T, E), torch.float32, dev, stream)
     else:
         _check("out", out, dev, _F32, (T, E))
+    _hold(stream, logits, ids, counts, grad_losses, mask, w, grad_w, out)
     _run("moe_balance_loss_backward", dev, stream, T, E, K, logits.data_ptr(), ids.data_ptr(), _ptr(mask),
          counts.data_ptr(), grad_losses.data_ptr(), _ptr(w), _ptr(grad_w), out.data_ptr())
     return out

@@ -179,6 +179,40 @@ def test_a_stream_of_another_device_is_refused():
         B._run("moe_fp8_quantize", torch.device("cuda", 0), stream)
 
 
+def test_a_given_stream_holds_every_tensor_of_the_call(monkeypatch):
+    """What a call on a stream of its own reads or writes is recorded on that
+    stream before anything is enqueued: the caller may drop it right after."""
+    held = set()
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: held.add((t.data_ptr(), s)))
+    monkeypatch.setattr(B, "_device", lambda t: t.device)
+    monkeypatch.setattr(B, "_empty", lambda shape, dtype, dev, stream: torch.empty(shape, dtype=dtype))
+    enqueued = []
+    monkeypatch.setattr(B, "_run", lambda *a: enqueued.append(set(held)))
+    f8, i32 = torch.float8_e4m3fn, torch.int32
+
+    def run(fn, *tensors, **named):
+        for stream in ("a stream", None):
+            held.clear()
+            fn(*tensors, **named, stream=stream)
+            given = [t for t in (*tensors, *named.values()) if isinstance(t, torch.Tensor)]
+            want = {(t.data_ptr(), stream) for t in given} if stream else set()
+            assert want <= enqueued[-1] and (stream or not enqueued[-1]), (fn.__name__, stream)
+
+    x = torch.zeros((4, 256), dtype=torch.bfloat16)
+    for fn, cols in ((B.fp8_quantize, 256), (B.fp8_swiglu, 128)):
+        run(fn, x, torch.zeros((4, cols), dtype=f8), torch.zeros((4, cols // 128)))
+        run(fn, x)
+    c, cs = torch.zeros((4, 256), dtype=f8), torch.zeros((4, 2))
+    w, ws = torch.zeros((2, 16, 256), dtype=f8), torch.zeros((2, 1, 2))
+    run(B.fp8_linear, c, cs, w[0], ws[0], out=torch.zeros((4, 16)))
+    run(B.fp8_grouped, c, cs, torch.zeros(3, dtype=i32), w, ws, row_index=torch.zeros(6, dtype=i32),
+        out=torch.zeros((6, 16)))
+    lg, ids, mask = torch.zeros((70, 8)), torch.zeros((70, 2), dtype=i32), torch.zeros(70, dtype=torch.uint8)
+    run(B.balance_loss, lg, ids, mask=mask, ws=torch.zeros(1 << 14, dtype=torch.uint8))
+    run(B.balance_loss_backward, lg, ids, torch.zeros(9, dtype=i32), torch.zeros(2), mask=mask, w=torch.zeros((70, 2)),
+        grad_w=torch.zeros((70, 2)), out=torch.zeros((70, 8)))
+
+
 def test_sizes_past_32_bits():
     B._int32(0, -1, 2 ** 31 - 1)
     for n in (2 ** 31, 2 ** 32 + 1, -2 ** 31 - 1):

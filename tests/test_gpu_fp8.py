@@ -409,6 +409,28 @@ def test_a_side_stream():
     assert torch.equal(got, want) and torch.equal(out, want)
 
 
+def test_inputs_dropped_after_a_call_on_a_given_stream():
+    """The call still waits on its stream when the caller drops its inputs: the
+    current stream does not get their memory."""
+    g = gen(4)
+    x, xs, w, ws = dev(*operands(512, 256, 4096, g))
+    want = B.fp8_linear(x, xs, w, ws)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    dropped = x.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)
+    got = B.fp8_linear(dropped, xs, w, ws, stream=s)
+    at = dropped.data_ptr()
+    del dropped
+    fresh = [torch.zeros_like(x) for _ in range(4)]
+    if not s.query():  # (the call has not run yet)
+        assert all(t.data_ptr() != at for t in fresh)
+    s.synchronize()
+    assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("tokens", [2, 40, 500])
 def test_captured_run_replays_as_eager(tokens):
     """quantize -> grouped -> swiglu -> grouped in one graph, replayed with new
