@@ -465,7 +465,40 @@ def balance_loss(logits: torch.Tensor, ids: torch.Tensor, mask=None, ws=None, st
     """moe_balance_loss of logits [T][E] fp32 and ids [T][K] int32, mask [T]
     uint8 or bool (tokens that count; None: all): (losses [2] fp32: balance,
     z; counts [E+1] int32: routes per expert, tokens that counted). ws: a
-    uint8 workspace of balance_workspace_bytes, allocated here if None."""
+    uint8 workspace of balance_workspace_bytes, allocated here if None.
+
+    Where logits requires a gradient, the losses carry theirs (of this call's
+    own counts, once, on the stream that was current here; without the router
+    weights' part, which is balance_loss_backward's). Not while a graph is
+    captured: there pass logits.detach() and call balance_loss_backward."""
+    if logits.requires_grad and torch.is_grad_enabled():
+        # (autograd would take the gradient to leaves whose accumulation is bound to the stream of an eager pass)
+        with torch.cuda.device(_device(logits)):
+            _need(not torch.cuda.is_current_stream_capturing(),
+                  "logits requires a gradient: in a capture pass logits.detach() and call balance_loss_backward")
+        return _BalanceLoss.apply(logits, ids, mask, ws, stream)
+    return _balance_loss(logits, ids, mask, ws, stream)
+
+
+class _BalanceLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids, mask, ws, stream):
+        losses, counts = _balance_loss(logits, ids, mask, ws, stream)
+        ctx.save_for_backward(logits, ids, counts, mask)
+        ctx.mark_non_differentiable(counts)
+        return losses, counts
+
+    @staticmethod
+    def backward(ctx, grad_losses, _):
+        if torch.is_grad_enabled():  # (create_graph: what comes back has no gradient of its own)
+            raise RuntimeError("balance_loss: cannot differentiate twice")
+        logits, ids, counts, mask = ctx.saved_tensors
+        # (counts may be of a given stream's pool)
+        _hold(torch.cuda.current_stream(counts.device), counts)
+        return balance_loss_backward(logits, ids, counts, grad_losses.contiguous(), mask), None, None, None, None
+
+
+def _balance_loss(logits, ids, mask, ws, stream):
     _need(logits.dim() == 2 and ids.dim() == 2, "logits, ids: need two dimensions")
     dev = _device(logits)
     (T, E), K = logits.shape, ids.shape[1]

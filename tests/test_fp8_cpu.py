@@ -173,6 +173,11 @@ def test_host_tensors_are_refused():
         B.balance_loss(torch.zeros((4, 8)), torch.zeros((4, 2), dtype=torch.int32))
 
 
+def test_host_logits_that_require_a_gradient_are_refused():
+    with pytest.raises(ValueError, match="GPU"):
+        B.balance_loss(torch.zeros((4, 8), requires_grad=True), torch.zeros((4, 2), dtype=torch.int32))
+
+
 def test_a_stream_of_another_device_is_refused():
     stream = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
     with pytest.raises(ValueError, match="stream"):

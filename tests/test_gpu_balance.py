@@ -225,6 +225,71 @@ def test_a_given_stream():
         assert torch.equal(losses, want[0]) and torch.equal(counts, want[1]) and torch.equal(g, want_g)
 
 
+@pytest.mark.parametrize("given_stream", [False, True])
+@pytest.mark.parametrize("T", [40, 700])
+def test_losses_carry_their_gradient(T, given_stream):
+    """Logits that require a gradient get it from the losses, as one term of a
+    larger loss too; where they do not, or no gradient is wanted, nothing is recorded."""
+    logits, ids, w, dw, mask = case(T, 20, 4, True)
+    gl = torch.tensor([0.7, 0.02])
+    grad, size = R.balance(logits, ids, mask, gl)[2:]
+    leaf = logits.cuda().requires_grad_()
+    plain, plain_c = B.balance_loss(leaf.detach(), ids.cuda(), mask.cuda())
+    assert not plain.requires_grad
+    with torch.no_grad():
+        assert not B.balance_loss(leaf, ids.cuda(), mask.cuda())[0].requires_grad
+    s = torch.cuda.Stream() if given_stream else None
+    if s:
+        s.wait_stream(torch.cuda.current_stream())
+    losses, counts = B.balance_loss(leaf, ids.cuda(), mask.cuda(), stream=s)
+    if s:
+        torch.cuda.current_stream().wait_stream(s)
+    assert losses.requires_grad and not counts.requires_grad
+    assert torch.equal(losses.detach(), plain) and torch.equal(counts, plain_c)
+    other = (leaf.square() * 0.25).sum()
+    ((losses * gl.cuda()).sum() + other).backward()
+    got = leaf.grad.cpu().double() - 0.5 * logits.double()
+    # (the sum of both parts in fp32: half a step of each and of the whole)
+    assert bool(((got - grad).abs() <= 64 * R.U24 * size + 2 * R.U24 * logits.double().abs() + 1e-30).all())
+    # through a router, one loss alone: its gradient is an expanded one
+    x, wr = torch.randn((T, 16), device="cuda"), torch.randn((20, 16), device="cuda", requires_grad=True)
+    lg = x @ wr.t()
+    B.balance_loss(lg, ids.cuda(), mask.cuda())[0].sum().backward()
+    one = torch.ones(2, device="cuda")
+    want = B.balance_loss_backward(lg.detach(), ids.cuda(), plain_c, one, mask.cuda()).t() @ x
+    assert torch.equal(wr.grad, want) or float((wr.grad - want).norm() / want.norm()) < 1e-6
+    B.balance_loss(leaf, ids.cuda(), mask.cuda())[0].sum()
+    again, _ = B.balance_loss(leaf, ids.cuda(), mask.cuda())
+    with pytest.raises(RuntimeError, match="differentiate twice|once_differentiable"):
+        (g,) = torch.autograd.grad(again.sum(), leaf, create_graph=True)
+        g.sum().backward()
+
+
+def test_no_gradient_is_recorded_in_a_capture():
+    """A captured call with logits that require a gradient is refused (an
+    eager pass over the same leaves may live); detached it runs, its gradient by its own call."""
+    logits, ids, _, _, mask = (cuda(t) for t in case(90, 20, 4, True))
+    leaf = logits.clone().requires_grad_()
+    living, counts = B.balance_loss(leaf, ids, mask)
+    one = torch.ones(2, device="cuda")
+    want = B.balance_loss_backward(logits, ids, counts, one, mask)
+    ws = torch.empty(B.balance_workspace_bytes(90, 20), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError, match="capture"):
+            B.balance_loss(leaf, ids, mask, ws)
+        losses, c = B.balance_loss(leaf.detach(), ids, mask, ws)
+        g = B.balance_loss_backward(leaf, ids, c, one, mask)
+    for _ in range(3):
+        g.zero_()
+        graph.replay()
+        assert torch.equal(g, want) and torch.equal(losses, living.detach())
+        torch.cuda.synchronize()
+    living.sum().backward()
+    assert torch.equal(leaf.grad, want)
+
+
 def test_refusals():
     logits, ids, w, dw, mask = (cuda(t) for t in case(70, 8, 2, True))
     counts = torch.zeros(9, dtype=torch.int32, device="cuda")
