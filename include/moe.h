@@ -436,7 +436,8 @@ int moe_fp8_grouped(int32_t rows, int32_t n_experts, int32_t N, int32_t K,
  *   losses     [2] fp32 out
  * Tokens whose logits are all -inf do not count either. With none that
  * counts (also T == 0) counts and losses are written as zeros. The same from
- * run to run, bit for bit.
+ * run to run, bit for bit. Whatever T is, at most about a hundred additions of
+ * one sum are in fp32 (the rest in 64 bits): within 1e-5 of the terms' sizes.
  * Backward, f held constant (counts may be sums over several calls or
  * processes, and are then the whole batch's):
  *   grad_logits[t][e] = grad_losses[0]/N * p (f_e - sum_j f_j p_j)

@@ -30,6 +30,12 @@ constexpr int kMaxE = 256;
 // Forward: 64 tokens at once, and at most one workgroup per CU, so that the one
 // workgroup that joins their sums reads little.
 constexpr int kFThreads = 1024, kFWaves = kFThreads / 64, kFTokens = kFThreads / 16, kFGroups = 256;
+// Tokens of a lane row that are summed in fp32 before their sum is taken over
+// into 64 bits: over thousands of like-signed additions an fp32 sum drifts (2^26
+// tokens: 2.5e-5 and 4.6e-5 of the two losses). Calls with fewer take a kernel
+// without the 64-bit sums, whose registers cost 0.4 .. 1 us (61 tokens 6.1 us
+// against 6.5, 32767 tokens 18.6 against 19.7).
+constexpr int kFRun = 32;
 constexpr int kBThreads = 256, kBTokens = kBThreads / 16;  // backward
 
 template <int CTRL>
@@ -101,7 +107,8 @@ __host__ __device__ inline size_t partial_pitch(int E) { return (static_cast<siz
 
 // One workgroup's tokens: those of index blockIdx.x, blockIdx.x + gridDim.x,
 // ... in units of kFTokens. ONE: the only workgroup, which writes the results.
-template <bool VEC, bool ONE>
+// LONG: a lane row may take more than kFRun tokens.
+template <bool VEC, bool ONE, bool LONG>
 __global__ __launch_bounds__(kFThreads) void balance_kernel(Balance p) {
   __shared__ int32_t cnt[kMaxE + 1];
   __shared__ float red[kFWaves][kMaxE + 1];
@@ -110,9 +117,24 @@ __global__ __launch_bounds__(kFThreads) void balance_kernel(Balance p) {
   for (int i = threadIdx.x; i <= kMaxE; i += kFThreads) cnt[i] = 0;
   __syncthreads();
   float acc[16], zz = 0.0f;
+  [[maybe_unused]] double far[16], far_z = 0.0;
+  [[maybe_unused]] int run = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+  for (int i = 0; i < 16; ++i) {
+    acc[i] = 0.0f;
+    far[i] = 0.0;
+  }
   for (int t0 = static_cast<int>(blockIdx.x) * kFTokens; t0 < p.T; t0 += static_cast<int>(gridDim.x) * kFTokens) {
+    if (LONG && run++ == kFRun) {
+      run = 1;
+      far_z += zz;
+      zz = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        far[i] += acc[i];
+        acc[i] = 0.0f;
+      }
+    }
     const int t = t0 + row;
     const bool in = t < p.T && (!p.mask || p.mask[t]);
     float v[16];
@@ -135,6 +157,11 @@ __global__ __launch_bounds__(kFThreads) void balance_kernel(Balance p) {
       zz = fmaf(lse, lse, zz);
       atomicAdd(&cnt[kMaxE], 1);
     }
+  }
+  if constexpr (LONG) {
+    zz = static_cast<float>(far_z + zz);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = static_cast<float>(far[i] + acc[i]);
   }
   // the wavefront's four tokens; lane row r keeps experts of i = 4r .. 4r+3
 #pragma unroll
@@ -365,21 +392,20 @@ size_t balance_workspace(int T, int E) {
   return G == 1 ? 0 : G * partial_pitch(E) * sizeof(Partial);
 }
 
+template <bool ONE, bool LONG>
+hipError_t launch_sums(const Balance& b, int G, hipStream_t st) {
+  if (b.E % 4 == 0)
+    MOE_LAUNCH((balance_kernel<true, ONE, LONG>), dim3(G), dim3(kFThreads), 0, st, b);
+  else
+    MOE_LAUNCH((balance_kernel<false, ONE, LONG>), dim3(G), dim3(kFThreads), 0, st, b);
+  return hipGetLastError();
+}
+
 hipError_t launch_balance_loss(const Balance& b, hipStream_t st) {
   const int G = balance_workgroups(b.T);
-  const bool vec = b.E % 4 == 0;
-  if (G == 1) {
-    if (vec)
-      MOE_LAUNCH((balance_kernel<true, true>), dim3(1), dim3(kFThreads), 0, st, b);
-    else
-      MOE_LAUNCH((balance_kernel<false, true>), dim3(1), dim3(kFThreads), 0, st, b);
-    return hipGetLastError();
-  }
-  if (vec)
-    MOE_LAUNCH((balance_kernel<true, false>), dim3(G), dim3(kFThreads), 0, st, b);
-  else
-    MOE_LAUNCH((balance_kernel<false, false>), dim3(G), dim3(kFThreads), 0, st, b);
-  hipError_t e = hipGetLastError();
+  if (G == 1) return launch_sums<true, false>(b, G, st);
+  const bool many = b.T > kFRun * kFTokens * kFGroups;
+  const hipError_t e = many ? launch_sums<false, true>(b, G, st) : launch_sums<false, false>(b, G, st);
   if (e != hipSuccess) return e;
   int log_c = 5;  // at least 32 pairs of experts, so at most 32 sets
   while ((2 << log_c) < b.E) ++log_c;

@@ -308,6 +308,26 @@ def test_refusals():
     assert e.value.status == B.MOE_EWORKSPACE
 
 
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("T,row", [(1 << 26, [0.3, 1.1, -0.7, 0.05]), ((1 << 22) + 77, [0.3, 1.1, -0.7]),
+                                   ((1 << 19) + 1, [0.3, 1.1])])
+def test_sums_over_many_tokens(T, row, masked):
+    """Equal tokens: their mean is the token's own value, and additions of one
+    sign do not drift."""
+    row = torch.tensor([row])
+    logits, ids = row.cuda().repeat(T, 1), torch.ones((T, 1), dtype=torch.int32, device="cuda")
+    mask = (torch.arange(T, device="cuda") % 3 > 0) if masked else None
+    n = T if mask is None else int(mask.sum())
+    losses, counts = B.balance_loss(logits, ids, mask)
+    assert counts.tolist() == ([0, n, 0, 0][:row.shape[1]] + [n])
+    p, lse = torch.softmax(row.double(), 1)[0], float(torch.logsumexp(row.double(), 1)[0])
+    # exponential and quotient 8 half steps, 32 tokens in fp32, joins of 2 + 16 + 40, f and the sum over the experts 16;
+    # lse^2: twice the logarithm's
+    rel = (8 + 32 + 2 + 16 + 40 + 16) * R.U24
+    assert abs(float(losses[0]) / (row.shape[1] * float(p[1])) - 1) <= rel
+    assert abs(float(losses[1]) / lse ** 2 - 1) <= rel + 16 * R.U24
+
+
 def test_offsets_past_32_bits():
     """Rows of logits and gradients beyond 2^32 bytes: the same values as near
     the start."""
