@@ -293,6 +293,13 @@ __device__ __forceinline__ void join_routes(int id, float gate, int l, float& su
   }
 }
 
+// LDS that other lanes of the wavefront wrote: the hardware keeps a wavefront's
+// accesses in order, and this keeps the compiler to it.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // GATE: with the gating weights' part. Each token has a row of LDS for it,
 // zero but for the experts its routes go to, which every lane reads beside
 // its logits; the rows belong to one wavefront, so nothing is waited for.
@@ -303,6 +310,7 @@ __global__ __launch_bounds__(kBThreads) void balance_backward_kernel(Balance p) 
   if constexpr (GATE) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) *reinterpret_cast<float4*>(&gates[row][q * 64 + l * 4]) = float4{0.f, 0.f, 0.f, 0.f};
+    wave_lds_order();
   }
   const float n = static_cast<float>(max(p.counts_in[p.E], 1));
   const float gb = p.dloss[0] / n, gz = 2.0f * p.dloss[1] / n;
@@ -354,15 +362,15 @@ __global__ __launch_bounds__(kBThreads) void balance_backward_kernel(Balance p) 
         bool first = id >= 0;
         join_routes(id, gate, l, joined, first);
         if (first) gates[row][id] = joined;
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_order();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float4 g = *reinterpret_cast<const float4*>(&gates[row][q * 64 + l * 4]);
           v[4 * q] += g.x, v[4 * q + 1] += g.y, v[4 * q + 2] += g.z, v[4 * q + 3] += g.w;
         }
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_order();
         if (first) gates[row][id] = 0.0f;
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_order();
       }
     }
     float* o = p.dlogits + static_cast<size_t>(t) * p.E;
