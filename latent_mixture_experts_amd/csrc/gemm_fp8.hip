@@ -18,8 +18,8 @@
 // sum is 1.5e-5 of the sums' norm off, which a bf16 rounding (half a step: up to
 // 2^-8 of the value) hides; where the terms cancel it may be all that is left. The
 // tiles with bf16 out take it, whatever bounds them, unless the caller asks for
-// fp32 sums (MOE_SUM_F32). Those, fp32 outs and the streaming kernel turn the
-// codes into bf16 (exact) and sum the block to fp32 by four bf16 MFMAs 16x16x32
+// fp32 sums (MOE_SUM_F32) or there are at most 16 dense rows. Those, fp32 outs and
+// the streaming kernel turn the codes into bf16 (exact) and sum the block to fp32 by four bf16 MFMAs 16x16x32
 // (measured: 1e-8 of the norm).
 #include <algorithm>
 #include <cmath>
@@ -730,20 +730,44 @@ int best_tile(const Fp8Gemm& g) {
   return best;
 }
 
+// Few rows and little to stream: the streaming kernel or the tiles. Per expert
+// (8 tokens on 4 experts 12.8 us against 12.0 .. 13.0) the streaming kernel,
+// until the weights fill the chip: there the tiles read faster, whole 128-byte
+// lines at a time (32 tokens' down projection 480 us against 510).
+//
+// Dense: a streaming wavefront reads the rows beside its 16 weight rows, so what
+// it costs grows with rows * K. Up to 4096 weight rows each of its workgroups has
+// a CU to itself and that is little; beyond, they share CUs, two on some and one
+// on others, and the tiles win but for the shortest products. In between: weight
+// rows a multiple of 4096 bytes apart meet on the same memory channels, which
+// costs the tiles a tenth (N = 28672: 4.1 TB/s at K = 8192, 5.0 at 7168), while the
+// CUs' last round of streaming workgroups is nearly full. The limits are where
+// the two cross over 18 widths N of 512 .. 28672 and 9 of K of 512 .. 14336 at
+// 1 .. 16 rows, weights from HBM (mean loss over the better of the two 0.6%, at
+// most 1.17 times). us, streaming kernel / tiles, fp32 sums:
+//   rows   4096x4096   4096x8192   5120x7168   8192x1024   8192x4096   16384x8192
+//      1   7.0 / 8.8    9.9 / 13.2  13.7 / 12.6   4.6 / 5.7    9.7 / 11.0  28.4 / 33.5
+//      4   7.2 / 8.9   10.7 / 13.4  14.7 / 12.7   4.6 / 5.7   10.6 / 10.9  31.9 / 33.7
+//     16   8.1 / 9.3   13.6 / 14.1  20.4 / 13.4   5.6 / 5.9   13.4 / 11.1  44.1 / 34.3
+bool streams(const Fp8Gemm& g) {
+  if (g.experts > 1) return true;
+  const int64_t values = static_cast<int64_t>(g.rows) * g.K;
+  if (g.N <= 4096) return values <= 128 << 10;
+  const int tiles = (g.N + 15) / 16, rounds = (tiles + 255) / 256;
+  if (g.K % 4096 == 0 && tiles * 8 >= rounds * 256 * 7) return values <= 16 << 10;
+  return values <= 8 << 10;
+}
+
 }  // namespace
 
-hipError_t launch_fp8_gemm(const Fp8Gemm& g, hipStream_t st) {
+hipError_t launch_fp8_gemm(const Fp8Gemm& call, hipStream_t st) {
+  Fp8Gemm g = call;
+  // Up to 16 dense rows are summed in fp32 by either kernel, so that few tokens'
+  // results do not go by the widths (tiles: 8192 x 4096 11.1 -> 11.5 us).
+  if (g.experts == 1 && g.rows <= 16) g.exact = true;
   const int groups = std::min(g.rows, g.experts);
   const int mean = (g.rows - 1) / g.experts + 1;
-  // Few rows and little to stream: the streaming kernel (N = 4096, K = 8192: one
-  // row 9 us against 11 with tiles, 8 rows 10.4 against 10.9; 8 tokens on 4
-  // experts 12.8 against 12.0 .. 13.0). Where the tiles fill the chip they read
-  // faster, whole 128-byte lines at a time (32 tokens' down projection 480 us
-  // against 510), and dense over many weight rows (N = 8192, K = 4096: 4 rows 9.3
-  // against 9.8, 16 rows 9.5 against 12.6) or a long K (N = 4096, K = 8192: 16
-  // rows 10.9 against 12.3).
-  const bool tiles = g.experts == 1 && ((g.N >= 8192 && g.rows > 4) || (g.K >= 8192 && g.rows > 8));
-  if (g.rows <= 64 && mean <= 16 && static_cast<int64_t>(groups) * ((g.N + 63) / 64) < 2048 && !tiles)
+  if (g.rows <= 64 && mean <= 16 && static_cast<int64_t>(groups) * ((g.N + 63) / 64) < 2048 && streams(g))
     return launch_stream(g, groups, st);
   switch (best_tile(g)) {
     case T32x32: return launch_tile<1, 2, 2, 1, 3, 4>(g, st);

@@ -251,6 +251,22 @@ def test_sums_in_fp32_lose_nothing(rows, n, k):
     R.assert_product(B.fp8_linear(*ops), *ops)
 
 
+# (rows, n, k) on both sides of where few rows go from the streaming kernel to the tiles
+FEW = [(1, 4112, 4096), (1, 4112, 4112), (1, 4097, 8208), (3, 5000, 1360), (3, 5000, 1376), (5, 8200, 1040), (16, 4200, 256),
+       (16, 4200, 272), (11, 4090, 8192), (13, 4090, 8192), (16, 500, 6144), (16, 500, 6160), (2, 20000, 2064), (16, 20000, 272),
+       (4, 8190, 4096), (5, 8190, 4096), (2, 7168, 8192), (3, 7168, 8192), (2, 7000, 8192)]
+
+
+@pytest.mark.parametrize("dtype,f32_sums", [(torch.bfloat16, False), (torch.bfloat16, True), (torch.float32, False)])
+@pytest.mark.parametrize("rows,n,k", FEW)
+def test_linear_few_rows(rows, n, k, dtype, f32_sums):
+    ops = dev(*operands(rows, n, k, gen(rows * 5 + n + k)))
+    R.assert_product(B.fp8_linear(*ops, dtype, f32_sums=f32_sums), *ops)
+    ops = dev(*R.cancelling(rows, n, k, gen(rows + n + k)))
+    got, want = B.fp8_linear(*ops, dtype, f32_sums=f32_sums), R.product(*ops)[0]
+    assert torch.equal(got, want.float().to(dtype))  # (a bf16 out of so few rows sums in fp32 anyway)
+
+
 GROUPS = [(90, 1, 2100, 272), (256, 20, 300, 144), (30, 40, 2100, 400), (60, 40, 3000, 144), (30, 60, 4200, 144),
           (30, 130, 2100, 272), (4, 600, 4200, 144), (8, 375, 700, 1040), (5, 2, 272, 640)]
 
