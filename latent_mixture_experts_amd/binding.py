@@ -323,10 +323,15 @@ def _pitch(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
+def _same_device(dev: torch.device, stream) -> None:
+    if stream.device != dev:
+        raise ValueError(f"the tensors are on {dev}, the stream on {stream.device}")
+
+
 def _run(what: str, dev: torch.device, stream, *args) -> None:
     fn = getattr(_lib or lib(), what)
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"the tensors are on {dev}, the stream on {stream.device}")
+    if stream is not None:
+        _same_device(dev, stream)
     # (the current stream's handle alone: building a torch.cuda.Stream costs as much as the launch)
     st = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
     if dev.index == torch._C._cuda_getDevice():
@@ -351,6 +356,7 @@ def _hold(stream, *tensors) -> None:
     """Memory of the call's tensors is not handed out again before the given
     stream has done the call, also when the caller drops them right after it."""
     if stream is not None:
+        _same_device(tensors[0].device, stream)
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)

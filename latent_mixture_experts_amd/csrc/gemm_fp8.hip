@@ -743,7 +743,7 @@ int best_tile(const Fp8Gemm& g) {
 // costs the tiles a tenth (N = 28672: 4.1 TB/s at K = 8192, 5.0 at 7168), while the
 // CUs' last round of streaming workgroups is nearly full. The limits are where
 // the two cross over 18 widths N of 512 .. 28672 and 9 of K of 512 .. 14336 at
-// 1 .. 16 rows, weights from HBM (mean loss over the better of the two 0.6%, at
+// 1 .. 16 rows, weights from HBM (mean loss over the better of the two 0.5%, at
 // most 1.17 times). us, streaming kernel / tiles, fp32 sums:
 //   rows   4096x4096   4096x8192   5120x7168   8192x1024   8192x4096   16384x8192
 //      1   7.0 / 8.8    9.9 / 13.2  13.7 / 12.6   4.6 / 5.7    9.7 / 11.0  28.4 / 33.5

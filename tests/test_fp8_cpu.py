@@ -188,19 +188,25 @@ def test_a_given_stream_holds_every_tensor_of_the_call(monkeypatch):
     """What a call on a stream of its own reads or writes is recorded on that
     stream before anything is enqueued: the caller may drop it right after."""
     held = set()
-    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: held.add((t.data_ptr(), s)))
     monkeypatch.setattr(B, "_device", lambda t: t.device)
     monkeypatch.setattr(B, "_empty", lambda shape, dtype, dev, stream: torch.empty(shape, dtype=dtype))
     enqueued = []
     monkeypatch.setattr(B, "_run", lambda *a: enqueued.append(set(held)))
     f8, i32 = torch.float8_e4m3fn, torch.int32
+    given_stream = types.SimpleNamespace(device=torch.device("cpu"), cuda_stream=0)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: held.add((t.data_ptr(), id(s))))
+    other = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
 
     def run(fn, *tensors, **named):
-        for stream in ("a stream", None):
+        held.clear()
+        with pytest.raises(ValueError, match="stream"):  # of another device: refused, nothing recorded on it
+            fn(*tensors, **named, stream=other)
+        assert not held, fn.__name__
+        for stream in (given_stream, None):
             held.clear()
             fn(*tensors, **named, stream=stream)
             given = [t for t in (*tensors, *named.values()) if isinstance(t, torch.Tensor)]
-            want = {(t.data_ptr(), stream) for t in given} if stream else set()
+            want = {(t.data_ptr(), id(stream)) for t in given} if stream else set()
             assert want <= enqueued[-1] and (stream or not enqueued[-1]), (fn.__name__, stream)
 
     x = torch.zeros((4, 256), dtype=torch.bfloat16)

@@ -463,6 +463,38 @@ def test_inputs_dropped_after_a_call_on_a_given_stream():
     assert torch.equal(got, want)
 
 
+def test_captured_on_a_given_stream():
+    """A call on a stream forked from the captured one and joined again, its
+    input made and dropped inside the capture."""
+    g = gen(6)
+    _, _, w, ws = dev(*operands(1, 256, 512, g))
+    x = torch.empty((70, 512), dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.Stream()
+
+    def run():
+        c, cs = B.fp8_quantize(x * 2)
+        here = torch.cuda.current_stream()
+        s.wait_stream(here)
+        out = B.fp8_linear(c, cs, w, ws, stream=s)
+        del c, cs
+        other = x * 3
+        here.wait_stream(s)
+        return out, other
+
+    x.copy_(activations(70, 512, g, torch.bfloat16))
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for seed in range(4):
+        x.copy_(activations(70, 512, gen(seed), torch.bfloat16))
+        graph.replay()
+        got = [t.clone() for t in out]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, run())), seed
+
+
 @pytest.mark.parametrize("tokens", [2, 40, 500])
 def test_captured_run_replays_as_eager(tokens):
     """quantize -> grouped -> swiglu -> grouped in one graph, replayed with new
