@@ -15,9 +15,10 @@
 // in registers over all tokens of a lane row, then are joined over the
 // workgroup in a fixed order, and over the workgroups by a second launch;
 // counts are integer atomics in LDS. Both are the same from run to run.
-// Bound by latency: 61 tokens of 16 experts 6.1 us forward (one workgroup), 4.7
-// backward; 4096 tokens of 256 experts 10.4 and 5.9; 32767 tokens 18.6 (the
-// join by one CU 7.6 of it) and 17.5, 3.8 TB/s.
+// Bound by latency (by events over a captured graph; a trace of single launches
+// says up to 1.7 us more each): 61 tokens of 16 experts 6.1 us forward (one
+// workgroup), 4.7 backward; 4096 tokens of 256 experts 10.4 and 6.0; 32767 tokens
+// 18.6 .. 19.2 (the join by one CU 7.6 of it) and 17.7, 3.8 TB/s.
 #include "balance.h"
 #include "device_common.h"
 #include "kernels.h"

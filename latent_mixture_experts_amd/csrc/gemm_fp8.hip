@@ -680,10 +680,12 @@ hipError_t launch_tile(const Fp8Gemm& g, hipStream_t st) {
 // The tiles: rows, weight rows, and what one block of K takes in ns: in the
 // first round of workgroups, and in each further one (the 32 x 64 ones share a CU
 // with others, so their further rounds overlap). `one`: for a single round
-// only, with stages of several blocks. Measured at K = 8192 in bf16 out; fp32 sums
-// take 1.2 times as long for 64 rows, 1.5 for 256, 1.7 for 2048, 2.1 for 4096. Small tiles win while they fit one
-// round: each has a CU to itself, and its stages wait on memory and on each
-// other, not on the matrix unit. N = 4096, K = 8192, us:
+// only, with stages of several blocks. Measured at N = 4096, K = 8192 in bf16 out
+// and taken to go the same way at other widths; fp32 sums take 1.2 times as long
+// for 64 rows, 1.5 for 256, 1.7 for 2048, 2.1 for 4096. Small tiles win while they
+// fit one round: each has a CU to itself. What bounds them is not the matrix unit:
+// their operands enter LDS at 11 .. 15 TB/s over the chip whichever tile is taken,
+// with stages that wait on memory and on each other. N = 4096, K = 8192, us:
 //   rows   32x32 one  32x64 one  64x64 one  64x128 one  32x64  64x128  128x128  128x256  256x256
 //     64       11        15         18          23        22      28       29       38       71
 //    128        -        15         18          23        22      28       35       53       71
@@ -693,8 +695,8 @@ hipError_t launch_tile(const Fp8Gemm& g, hipStream_t st) {
 //   4096        -         -          -           -         -       -        -      155      117
 // (48 x 32: 33 rows of N = 8192, K = 4096 10.2 us against 11.0 with 32 x 64.)
 // 144 x 256 stands for experts of about 128 rows, half of which would take a
-// second, nearly empty tile of 128 (4096 tokens' down projection 1115 -> 1053 us;
-// experts of 109 rows 1014 against 1011).
+// second, nearly empty tile of 128 (4096 tokens' down projection 6% less time than
+// with 128 x 256, experts of 109 rows the same).
 struct TileShape {
   int rows, cols, first_ns, more_ns;
   bool one;
@@ -716,7 +718,7 @@ int best_tile(const Fp8Gemm& g) {
   for (int i = 0; i < kNTiles; ++i) {
     const TileShape& t = kTiles[i];
     // 256 x 256: its sums fill the registers, no room for bf16 operands; and
-    // partly filled ones waste most (experts of 128 rows: 1153 us against 1051)
+    // partly filled ones waste most (experts of 128 rows: 10% more time)
     if (t.rows == 256 && (g.exact || (g.experts > 1 && mean < 512))) continue;
     const double tiles = groups * std::ceil(rows / t.rows) * std::ceil(static_cast<double>(g.N) / t.cols);
     if (t.one && tiles > 256.0) continue;

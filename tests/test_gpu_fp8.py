@@ -142,6 +142,22 @@ def test_swiglu_of_gates_up_to_the_exponentials_overflow(dtype):
     assert bool((codes.float() == -448).all())
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_swiglu_of_large_and_tiny_gates(dtype):
+    """silu from 2^-80 to the type's largest value, and zeros of both signs."""
+    gate = torch.tensor([2.0 ** -80, -2.0 ** -80, 1e-20, -1e-7, 0.5, -1.25, 15.0, 20.0, 90.0, 199.0, 201.0, 1e10, 2e30, 3e38,
+                         0.0, -0.0], dtype=dtype)
+    gu = torch.cat([gate[:, None].expand(-1, 128), torch.full((gate.numel(), 128), -1.0, dtype=dtype)], 1)
+    codes, scales = B.fp8_swiglu(gu.cuda())
+    d = gate.double()
+    h = d * torch.sigmoid(d)
+    amax = h.abs().clamp_min(R.TINY)
+    # (h: under 16 half steps, the scale's quotient one more)
+    assert bool(((scales[:, 0].cpu().double() * 448 / amax - 1).abs() <= 18 * R.U24).all())
+    want = torch.where(h == 0, 0.0, torch.where(h > 0, -448.0, 448.0))
+    assert bool((codes.cpu().double() == want[:, None]).all())
+
+
 def test_swiglu_non_finite():
     gu = torch.ones((4, 256))
     gu[0, 3] = float("nan")
