@@ -284,6 +284,8 @@ def workspace_view(d: MoeDims, T: int, ws: torch.Tensor, which: str, dtype, shap
 # torch.cuda.Stream). What they allocate then belongs to that stream, and what
 # they were given may be dropped once they return; order between the streams
 # (inputs written before, results read after, there or elsewhere) is the caller's.
+# Only balance_loss is recorded for autograd; the 8-bit calls have no gradient,
+# and what they return requires none.
 TYPE_BF16, TYPE_F32 = 0, 1  # MOE_TYPE_*
 SUM_F32 = 0x100  # MOE_SUM_F32
 _FLOATS = {torch.bfloat16: TYPE_BF16, torch.int16: TYPE_BF16, torch.float32: TYPE_F32}  # int16: bf16 bits
