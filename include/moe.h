@@ -463,6 +463,119 @@ int moe_balance_loss_backward(int32_t T, int32_t n_experts, int32_t top_k,
                               const float *grad_topk_w, float *grad_logits,
                               void *hip_stream);
 
+/*
+ * 4-bit rows and their products (MXFP4, as the layer's expert weights are
+ * stored): E2M1 codes, two per byte, the first in the low half, with one E8M0
+ * scale byte (2^(b-127); 255: NaN) per 32 consecutive values of a row, for the
+ * rows and the weights. They stand beside the layer's W4A16 projections, for
+ * rows in 4 bits too (W4A4).
+ *
+ * Widths (cols, K) are multiples of 32 up to 65536, N up to 65536, rows below
+ * 2^28. Codes and x 16-byte aligned, rows of x 16-byte aligned (pitches in
+ * elements, at most 2^22; a pitch of codes in bytes); scales any address;
+ * offsets, indices and out need the alignment of their type only. Zero rows
+ * are a no-op.
+ *
+ * moe_fp4_quantize: x [rows][cols] (pitch ldx) of x_type to
+ *   codes  [rows][cols/2]   e2m1(x / X), nearest, ties to even
+ *   scales [rows][cols/32]  X = 2^max(e-2, -126), e the exponent of the group's
+ *                           largest |x| rounded to two significant bits
+ * so that |x / X| < 7 and every value is within half a step of E2M1. A group
+ * that holds a NaN or an infinity gets scale 255 and codes 0: all of it NaN.
+ * moe_fp4_swiglu: the same of h = silu(gate) * up in fp32; a row of gate_up
+ * holds inter gate values, then inter up values.
+ * moe_fp4_dequantize: codes and scales to out [rows][cols] (pitch ldo) of
+ * out_type, exactly (past bf16's or fp32's range: infinite).
+ */
+int moe_fp4_quantize(int32_t rows, int32_t cols, const void *x, int64_t ldx,
+                     int32_t x_type, uint8_t *codes, uint8_t *scales,
+                     void *hip_stream);
+int moe_fp4_swiglu(int32_t rows, int32_t inter, const void *gate_up, int64_t ld,
+                   int32_t type, uint8_t *codes, uint8_t *scales,
+                   void *hip_stream);
+int moe_fp4_dequantize(int32_t rows, int32_t cols, const uint8_t *codes,
+                       const uint8_t *scales, void *out, int64_t ldo,
+                       int32_t out_type, void *hip_stream);
+
+/* moe_fp4_linear: out[t][n] = sum over groups b of 32 of
+ *     2^(x_scales[t][b] + w_scales[n][b] - 254) * sum_{k in b} x[t][k] * w[n][k]
+ *   x [T][K] codes (pitch ldx bytes), x_scales [T][K/32],
+ *   w [N][K] codes, w_scales [N][K/32],
+ *   out [T][N] (pitch ldo) of out_type, rounded once from an fp32 sum. (A
+ *   group's sum is exact; the order in which the groups are added goes by the
+ *   sizes.)
+ * moe_fp4_grouped: the same product for every expert over its own rows, with
+ * moe_fp8_grouped's offsets, row_index, index_div and x_rows:
+ *   x [x_rows][K], x_scales [x_rows][K/32], w [E][N][K], w_scales [E][N][K/32]
+ *   (the layer's w13 and w2 as they are), out [rows][N].
+ * n_experts <= 256; with row_index x_rows * ldx < 2^31. */
+int moe_fp4_linear(int32_t T, int32_t N, int32_t K, const uint8_t *x,
+                   int64_t ldx, const uint8_t *x_scales, const uint8_t *w,
+                   const uint8_t *w_scales, void *out, int64_t ldo,
+                   int32_t out_type, void *hip_stream);
+int moe_fp4_grouped(int32_t rows, int32_t n_experts, int32_t N, int32_t K,
+                    const int32_t *offsets, const int32_t *row_index,
+                    int32_t index_div, int32_t x_rows, const uint8_t *x,
+                    int64_t ldx, const uint8_t *x_scales, const uint8_t *w,
+                    const uint8_t *w_scales, void *out, int64_t ldo,
+                    int32_t out_type, void *hip_stream);
+
+/*
+ * The way into expert order and back, for rows of any router: what
+ * moe_latent_forward does inside, as calls of their own, with gradients.
+ *
+ * moe_sort_routes: the routes r = t*K + k of topk_ids [T][K] int32, grouped by
+ * expert. This process holds experts first_expert .. first_expert+n_experts-1;
+ * routes to others (or to none: padding) are left out.
+ *   expert_offsets [n_experts+1] int32 out: exclusive prefix sums of the
+ *                    routes per expert; [n_experts]: routes that are here
+ *   sorted_routes  [T*K] int32 out: route ids by expert, ascending within one;
+ *                    behind the last: -1
+ *   positions      [T][K] int32 out: where sorted_routes holds the route, or -1
+ * workspace: moe_sort_workspace_bytes (0 for few routes: may be NULL).
+ */
+size_t moe_sort_workspace_bytes(int32_t T, int32_t n_experts, int32_t top_k);
+int moe_sort_routes(int32_t T, int32_t n_experts, int32_t top_k,
+                    const int32_t *topk_ids, int32_t first_expert,
+                    int32_t *expert_offsets, int32_t *sorted_routes,
+                    int32_t *positions, void *workspace, size_t workspace_bytes,
+                    void *hip_stream);
+
+/* moe_gather_rows: out[positions[t][k]] = x[t], x [T][cols] (pitch ldx), out
+ * [rows][cols] (pitch ldo), both of type. Its gradient is moe_combine_rows of
+ * the rows' gradients without weights.
+ * moe_combine_rows: out[t] = sum_k topk_w[t][k] * x[positions[t][k]] in fp32,
+ * k ascending, rounded once; x [rows][cols] (pitch ldx) of type, topk_w [T][K]
+ * fp32 or NULL (all 1), out [T][cols] (pitch ldo) of out_type. A token with no
+ * position gets zeros.
+ * moe_combine_rows_backward, for grad_out [T][cols] (pitch ldg) of grad_type:
+ *   grad_rows[positions[t][k]] = topk_w[t][k] * grad_out[t]   [rows][cols] of
+ *                                type (pitch ldr), or NULL
+ *   grad_w[t][k] = sum_c x[positions[t][k]][c] * grad_out[t][c]   [T][K] fp32,
+ *                  or NULL (x is then not read and may be NULL); 0 for no position
+ * Positions outside [0, rows) are none; no two may be the same row (that row
+ * is then unspecified). n_taken: NULL, and rows that no position names are left
+ * as they were; or a device int32 (moe_sort_routes' expert_offsets[n_experts]),
+ * and rows from *n_taken on become zeros.
+ * cols 1 .. 65536, top_k <= 8, T * top_k and rows below 2^28, pitches in
+ * elements up to 2^22. Pointers need the alignment of their type only (rows of
+ * a multiple of 8 values, all 16-byte aligned, are fastest). */
+int moe_gather_rows(int32_t T, int32_t top_k, int32_t rows, int32_t cols,
+                    const void *x, int64_t ldx, int32_t type,
+                    const int32_t *positions, const int32_t *n_taken, void *out,
+                    int64_t ldo, void *hip_stream);
+int moe_combine_rows(int32_t T, int32_t top_k, int32_t rows, int32_t cols,
+                     const void *x, int64_t ldx, int32_t type,
+                     const int32_t *positions, const float *topk_w, void *out,
+                     int64_t ldo, int32_t out_type, void *hip_stream);
+int moe_combine_rows_backward(int32_t T, int32_t top_k, int32_t rows,
+                              int32_t cols, const void *grad_out, int64_t ldg,
+                              int32_t grad_type, const void *x, int64_t ldx,
+                              int32_t type, const int32_t *positions,
+                              const float *topk_w, const int32_t *n_taken,
+                              void *grad_rows, int64_t ldr, float *grad_w,
+                              void *hip_stream);
+
 /* Their argument checks alone (callable without a GPU). */
 int moe_fp8_quantize_validate(int32_t rows, int32_t cols, const void *x,
                               int64_t ldx, int32_t x_type, const uint8_t *codes,
@@ -495,6 +608,46 @@ int moe_balance_loss_backward_validate(int32_t T, int32_t n_experts,
                                        const float *topk_w,
                                        const float *grad_topk_w,
                                        const float *grad_logits);
+int moe_fp4_quantize_validate(int32_t rows, int32_t cols, const void *x,
+                              int64_t ldx, int32_t x_type, const uint8_t *codes,
+                              const uint8_t *scales);
+int moe_fp4_swiglu_validate(int32_t rows, int32_t inter, const void *gate_up,
+                            int64_t ld, int32_t type, const uint8_t *codes,
+                            const uint8_t *scales);
+int moe_fp4_dequantize_validate(int32_t rows, int32_t cols, const uint8_t *codes,
+                                const uint8_t *scales, const void *out,
+                                int64_t ldo, int32_t out_type);
+int moe_fp4_linear_validate(int32_t T, int32_t N, int32_t K, const uint8_t *x,
+                            int64_t ldx, const uint8_t *x_scales,
+                            const uint8_t *w, const uint8_t *w_scales,
+                            const void *out, int64_t ldo, int32_t out_type);
+int moe_fp4_grouped_validate(int32_t rows, int32_t n_experts, int32_t N,
+                             int32_t K, const int32_t *offsets,
+                             const int32_t *row_index, int32_t index_div,
+                             int32_t x_rows, const uint8_t *x, int64_t ldx,
+                             const uint8_t *x_scales, const uint8_t *w,
+                             const uint8_t *w_scales, const void *out,
+                             int64_t ldo, int32_t out_type);
+int moe_sort_routes_validate(int32_t T, int32_t n_experts, int32_t top_k,
+                             const int32_t *topk_ids, int32_t first_expert,
+                             const int32_t *expert_offsets,
+                             const int32_t *sorted_routes,
+                             const int32_t *positions, const void *workspace,
+                             size_t workspace_bytes);
+int moe_gather_rows_validate(int32_t T, int32_t top_k, int32_t rows,
+                             int32_t cols, const void *x, int64_t ldx,
+                             int32_t type, const int32_t *positions,
+                             const int32_t *n_taken, const void *out, int64_t ldo);
+int moe_combine_rows_validate(int32_t T, int32_t top_k, int32_t rows,
+                              int32_t cols, const void *x, int64_t ldx,
+                              int32_t type, const int32_t *positions,
+                              const float *topk_w, const void *out, int64_t ldo,
+                              int32_t out_type);
+int moe_combine_rows_backward_validate(
+    int32_t T, int32_t top_k, int32_t rows, int32_t cols, const void *grad_out,
+    int64_t ldg, int32_t grad_type, const void *x, int64_t ldx, int32_t type,
+    const int32_t *positions, const float *topk_w, const int32_t *n_taken,
+    const void *grad_rows, int64_t ldr, const float *grad_w);
 
 /* Host-side evaluation of the tile orders of the prefill kernels (tests
  * check them over many shapes; no device work). For launch `kind`:

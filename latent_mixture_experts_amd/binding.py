@@ -110,6 +110,17 @@ def lib():
             "moe_fp8_linear": [_i32, _i32, _i32, _vp, i64, _vp, _vp, _vp, _vp, i64, _i32],
             "moe_fp8_grouped": [_i32, _i32, _i32, _i32, _vp, _vp, _i32, _i32, _vp, i64, _vp, _vp,
                                 _vp, _vp, i64, _i32],
+            "moe_fp4_quantize": [_i32, _i32, _vp, i64, _i32, _vp, _vp],
+            "moe_fp4_swiglu": [_i32, _i32, _vp, i64, _i32, _vp, _vp],
+            "moe_fp4_dequantize": [_i32, _i32, _vp, _vp, _vp, i64, _i32],
+            "moe_fp4_linear": [_i32, _i32, _i32, _vp, i64, _vp, _vp, _vp, _vp, i64, _i32],
+            "moe_fp4_grouped": [_i32, _i32, _i32, _i32, _vp, _vp, _i32, _i32, _vp, i64, _vp, _vp,
+                                _vp, _vp, i64, _i32],
+            "moe_sort_routes": [_i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _sz],
+            "moe_gather_rows": [_i32, _i32, _i32, _i32, _vp, i64, _i32, _vp, _vp, _vp, i64],
+            "moe_combine_rows": [_i32, _i32, _i32, _i32, _vp, i64, _i32, _vp, _vp, _vp, i64, _i32],
+            "moe_combine_rows_backward": [_i32, _i32, _i32, _i32, _vp, i64, _i32, _vp, i64, _i32, _vp, _vp,
+                                          _vp, _vp, i64, _vp],
             "moe_balance_loss": [_i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz],
             "moe_balance_loss_backward": [_i32, _i32, _i32] + [_vp] * 8,
         }.items():
@@ -117,6 +128,8 @@ def lib():
                 fn.restype, fn.argtypes = ctypes.c_int, args + more
         L.moe_balance_workspace_bytes.restype = _sz
         L.moe_balance_workspace_bytes.argtypes = [_i32, _i32]
+        L.moe_sort_workspace_bytes.restype = _sz
+        L.moe_sort_workspace_bytes.argtypes = [_i32, _i32, _i32]
         L.moe_status_string.restype = ctypes.c_char_p
         L.moe_status_string.argtypes = [ctypes.c_int]
         L.moe_last_hip_error.restype = ctypes.c_int
@@ -277,15 +290,15 @@ def workspace_view(d: MoeDims, T: int, ws: torch.Tensor, which: str, dtype, shap
     return ws[off:off + nb].view(dtype).view(shape)
 
 
-# ---- 8-bit rows, their products, the balance loss --------------------------
+# ---- 8-bit and 4-bit rows, their products, expert order, the balance loss ---
 # These take their sizes from the tensors, so they check them: a wrong shape,
 # type, layout or device raises ValueError before anything is enqueued. They
 # run on the tensors' device, on its current stream unless one is given (a
 # torch.cuda.Stream). What they allocate then belongs to that stream, and what
 # they were given may be dropped once they return; order between the streams
 # (inputs written before, results read after, there or elsewhere) is the caller's.
-# Only balance_loss is recorded for autograd; the 8-bit calls have no gradient,
-# and what they return requires none.
+# Only balance_loss, gather_rows and combine_rows are recorded for autograd; the
+# 8-bit and 4-bit calls have no gradient, and what they return requires none.
 TYPE_BF16, TYPE_F32 = 0, 1  # MOE_TYPE_*
 SUM_F32 = 0x100  # MOE_SUM_F32
 _FLOATS = {torch.bfloat16: TYPE_BF16, torch.int16: TYPE_BF16, torch.float32: TYPE_F32}  # int16: bf16 bits
@@ -462,6 +475,304 @@ def fp8_grouped(x: torch.Tensor, x_scales: torch.Tensor, offsets: torch.Tensor, 
          x_rows, x.data_ptr(), _pitch(x), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
          out.data_ptr(), _pitch(out), _FLOATS[out.dtype] | SUM_F32 if f32_sums else _FLOATS[out.dtype])
     return out
+
+
+_NIBBLES, _E8M0 = (torch.uint8,), (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _fp4_quantize(what: str, x: torch.Tensor, cols: int, codes, scales, stream):
+    dev = _device(x)
+    rows = x.shape[0]
+    _int32(rows | cols)
+    _check("x", x, dev, _ANY_FLOAT, (rows, x.shape[1]), pitched=True)
+    _need(cols % 32 == 0, f"x: needs a width in groups of 32, got {cols}")
+    if codes is None:
+        codes = _empty((rows, cols // 2), torch.uint8, dev, stream)
+    else:
+        _check("codes", codes, dev, _NIBBLES, (rows, cols // 2))
+    if scales is None:
+        scales = _empty((rows, cols // 32), torch.uint8, dev, stream)
+    else:
+        _check("scales", scales, dev, _E8M0, (rows, cols // 32))
+    _hold(stream, x, codes, scales)
+    _run(what, dev, stream, rows, cols, x.data_ptr(), _pitch(x), _FLOATS[x.dtype], codes.data_ptr(),
+         scales.data_ptr())
+    return codes, scales
+
+
+def fp4_quantize(x: torch.Tensor, codes=None, scales=None, stream=None):
+    """moe_fp4_quantize of x [rows][cols] (bf16 or fp32, rows at any pitch):
+    (codes [rows][cols/2] uint8, two E2M1 values a byte; scales [rows][cols/32]
+    uint8, E8M0): the layer's MXFP4, also for its weights."""
+    _need(x.dim() == 2, "x: needs two dimensions")
+    return _fp4_quantize("moe_fp4_quantize", x, x.shape[1], codes, scales, stream)
+
+
+def fp4_swiglu(gate_up: torch.Tensor, codes=None, scales=None, stream=None):
+    """moe_fp4_swiglu of gate_up [rows][2 * inter] (gate values, then up
+    values): silu(gate) * up as fp4_quantize gives it."""
+    _need(gate_up.dim() == 2 and gate_up.shape[1] % 2 == 0, "gate_up: needs two dimensions, the second even")
+    return _fp4_quantize("moe_fp4_swiglu", gate_up, gate_up.shape[1] // 2, codes, scales, stream)
+
+
+def fp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, out_dtype=torch.bfloat16, out=None,
+                   stream=None) -> torch.Tensor:
+    """moe_fp4_dequantize: the values [rows][cols] of codes [rows][cols/2] and
+    scales [rows][cols/32], of out_dtype or into out (rows at any pitch)."""
+    _need(codes.dim() == 2, "codes: needs two dimensions")
+    dev = _device(codes)
+    rows, cols = codes.shape[0], 2 * codes.shape[1]
+    _int32(rows | cols)
+    _check("codes", codes, dev, _NIBBLES, (rows, cols // 2))
+    _check("scales", scales, dev, _E8M0, (rows, cols // 32))
+    out = _out(out, rows, cols, out_dtype, dev, stream)
+    _hold(stream, codes, scales, out)
+    _run("moe_fp4_dequantize", dev, stream, rows, cols, codes.data_ptr(), scales.data_ptr(), out.data_ptr(),
+         _pitch(out), _FLOATS[out.dtype])
+    return out
+
+
+def fp4_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+               out_dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+    """moe_fp4_linear: x [T][K/2] with x_scales [T][K/32] times w [N][K/2] with
+    w_scales [N][K/32], as fp4_quantize gives them -> [T][N] of out_dtype, or
+    into out. Rows of x and out at any pitch."""
+    _need(x.dim() == 2 and w.dim() == 2, "x, w: need two dimensions")
+    dev = _device(x)
+    (T, half), N = x.shape, w.shape[0]
+    K = 2 * half
+    _int32(T | K | N)
+    _check("x", x, dev, _NIBBLES, (T, half), pitched=True)
+    _check("x_scales", x_scales, dev, _E8M0, (T, K // 32))
+    _check("w", w, dev, _NIBBLES, (N, half))
+    _check("w_scales", w_scales, dev, _E8M0, (N, K // 32))
+    out = _out(out, T, N, out_dtype, dev, stream)
+    _hold(stream, x, x_scales, w, w_scales, out)
+    _run("moe_fp4_linear", dev, stream, T, N, K, x.data_ptr(), _pitch(x), x_scales.data_ptr(), w.data_ptr(),
+         w_scales.data_ptr(), out.data_ptr(), _pitch(out), _FLOATS[out.dtype])
+    return out
+
+
+def fp4_grouped(x: torch.Tensor, x_scales: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
+                w_scales: torch.Tensor, out_dtype=torch.bfloat16, row_index=None, index_div: int = 1,
+                out=None, stream=None) -> torch.Tensor:
+    """moe_fp4_grouped: rows offsets[e] .. offsets[e+1]-1 times expert e's
+    weights, w [E][N][K/2] with w_scales [E][N][K/32] (the layer's w13 and w2 as
+    they are), offsets [E+1] int32. The rows are those of x, or with row_index
+    [rows] int32 row row_index[i] // index_div of x for output row i. Rows of
+    out that no expert takes are left as they are (as allocated, without out)."""
+    _need(x.dim() == 2 and w.dim() == 3, "x: needs two dimensions, w three")
+    dev = _device(x)
+    (x_rows, half), (E, N, _) = x.shape, w.shape
+    K = 2 * half
+    rows = x_rows if row_index is None else row_index.numel()
+    _int32(rows | x_rows | K | E | N, index_div)
+    _check("x", x, dev, _NIBBLES, (x_rows, half), pitched=True)
+    _check("x_scales", x_scales, dev, _E8M0, (x_rows, K // 32))
+    _check("offsets", offsets, dev, _I32, (E + 1,))
+    _check("w", w, dev, _NIBBLES, (E, N, half))
+    _check("w_scales", w_scales, dev, _E8M0, (E, N, K // 32))
+    if row_index is not None:
+        _check("row_index", row_index, dev, _I32, (rows,))
+    out = _out(out, rows, N, out_dtype, dev, stream)
+    _hold(stream, x, x_scales, offsets, w, w_scales, row_index, out)
+    _run("moe_fp4_grouped", dev, stream, rows, E, N, K, offsets.data_ptr(), _ptr(row_index), index_div,
+         x_rows, x.data_ptr(), _pitch(x), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
+         out.data_ptr(), _pitch(out), _FLOATS[out.dtype])
+    return out
+
+
+def sort_workspace_bytes(T: int, n_experts: int, top_k: int) -> int:
+    _int32(T, n_experts, top_k)
+    return int(lib().moe_sort_workspace_bytes(T, n_experts, top_k))
+
+
+def sort_routes(ids: torch.Tensor, n_experts: int, first: int = 0, ws=None, stream=None) -> dict:
+    """moe_sort_routes of ids [T][K] int32, for the experts first ..
+    first + n_experts - 1 (routes to others are left out): a dict of int32
+    tensors, offsets [n_experts+1], sorted [T*K], positions [T][K]. ws: a uint8
+    workspace of sort_workspace_bytes, allocated here if None."""
+    _need(ids.dim() == 2, "ids: needs two dimensions")
+    dev = _device(ids)
+    T, K = ids.shape
+    _int32(T | K, n_experts, first)
+    _check("ids", ids, dev, _I32, (T, K))
+    _need(n_experts >= 0, "n_experts: negative")
+    if ws is None:
+        n = sort_workspace_bytes(T, n_experts, K)
+        ws = _empty(n, torch.uint8, dev, stream) if n else None
+    else:
+        _check("ws", ws, dev, (torch.uint8,), (ws.numel(),))
+    offsets = _empty(n_experts + 1, torch.int32, dev, stream)
+    order = _empty(T * K, torch.int32, dev, stream)
+    positions = _empty((T, K), torch.int32, dev, stream)
+    _hold(stream, ids, ws)
+    _run("moe_sort_routes", dev, stream, T, n_experts, K, ids.data_ptr(), first, offsets.data_ptr(),
+         order.data_ptr(), positions.data_ptr(), _ptr(ws), ws.numel() if ws is not None else 0)
+    return dict(offsets=offsets, sorted=order, positions=positions)
+
+
+def _positions(routes: dict, dev: torch.device, zero_rest: bool):
+    """(positions, device address of the count of rows that are taken, or None; the tensor that holds it)."""
+    positions, offsets = routes["positions"], routes["offsets"]
+    _need(positions.dim() == 2, "positions: needs two dimensions")
+    _check("positions", positions, dev, _I32, tuple(positions.shape))
+    if not zero_rest:
+        return positions, None, None
+    _check("offsets", offsets, dev, _I32, (offsets.numel(),))
+    _need(offsets.numel() > 0, "offsets: empty")
+    return positions, offsets.data_ptr() + 4 * (offsets.numel() - 1), offsets
+
+
+def _no_capture(t: torch.Tensor, what: str, instead: str) -> None:
+    # (autograd would take the gradient to leaves whose accumulation is bound to the stream of an eager pass)
+    with torch.cuda.device(_device(t)):
+        _need(not torch.cuda.is_current_stream_capturing(),
+              f"{what} requires a gradient: in a capture pass {what}.detach() and call {instead}")
+
+
+def _once(what: str) -> None:
+    if torch.is_grad_enabled():  # (create_graph: what comes back has no gradient of its own)
+        raise RuntimeError(f"{what}: cannot differentiate twice")
+    if torch.cuda.is_current_stream_capturing():  # (as _no_capture, for a forward pass that was not captured)
+        raise RuntimeError(f"{what}: its gradient cannot be captured, call {what}_backward")
+
+
+def gather_rows(x: torch.Tensor, routes: dict, out=None, zero_rest: bool = False, stream=None) -> torch.Tensor:
+    """moe_gather_rows: x [T][cols] (bf16 or fp32, rows at any pitch) into the
+    order of routes (sort_routes' dict; offsets and positions are read): [T*K]
+    rows, or into out [rows][cols]. Rows behind the last route are left as they
+    are (as allocated, without out), or zeros with zero_rest.
+
+    Where x requires a gradient, the rows carry it (once, on the stream that was
+    current here), and those behind the last route are zeros; out is not taken.
+    Not while a graph is captured: there pass x.detach() and call
+    gather_rows_backward."""
+    if x.requires_grad and torch.is_grad_enabled():
+        _no_capture(x, "x", "gather_rows_backward")
+        _need(out is None, "out: not with an x that requires a gradient")
+        return _GatherRows.apply(x, routes["offsets"], routes["positions"], stream)
+    return _gather_rows(x, routes, out, zero_rest, stream)
+
+
+def _gather_rows(x, routes, out, zero_rest, stream):
+    _need(x.dim() == 2, "x: needs two dimensions")
+    dev = _device(x)
+    positions, taken, offsets = _positions(routes, dev, zero_rest)
+    (T, K), cols = positions.shape, x.shape[1]
+    rows = T * K if out is None else out.shape[0]
+    _int32(T | K | rows | cols)
+    _check("x", x, dev, _ANY_FLOAT, (T, cols), pitched=True)
+    if out is None:
+        out = _empty((rows, cols), x.dtype, dev, stream)
+    else:
+        _check("out", out, dev, (x.dtype,), (rows, cols), pitched=True)
+    _hold(stream, x, positions, offsets, out)
+    _run("moe_gather_rows", dev, stream, T, K, rows, cols, x.data_ptr(), _pitch(x), _FLOATS[x.dtype],
+         positions.data_ptr(), taken, out.data_ptr(), _pitch(out))
+    return out
+
+
+def gather_rows_backward(grad_rows: torch.Tensor, routes: dict, out_dtype=None, out=None, stream=None) -> torch.Tensor:
+    """The gradient [T][cols] of gather_rows' x: the sum of its rows' gradients
+    (moe_combine_rows without weights)."""
+    return _combine_rows(grad_rows, routes, None, out_dtype, out, stream)
+
+
+class _GatherRows(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, offsets, positions, stream):
+        ctx.save_for_backward(offsets, positions)
+        return _gather_rows(x, dict(offsets=offsets, positions=positions), None, True, stream)
+
+    @staticmethod
+    def backward(ctx, grad_rows):
+        _once("gather_rows")
+        offsets, positions = ctx.saved_tensors
+        _hold(torch.cuda.current_stream(positions.device), positions)
+        grad = _combine_rows(grad_rows.contiguous(), dict(offsets=offsets, positions=positions), None, None, None, None)
+        return grad, None, None, None
+
+
+def combine_rows(rows: torch.Tensor, routes: dict, w=None, out_dtype=None, out=None, stream=None) -> torch.Tensor:
+    """moe_combine_rows: per token the sum of its routes' rows [rows][cols] (bf16
+    or fp32, at any pitch), weighted with w [T][K] fp32 (None: 1): [T][cols] of
+    out_dtype (None: that of rows), or into out.
+
+    Where rows or w require a gradient, the result carries it (once, on the
+    stream that was current here); rows behind the last route get zeros. out is
+    not taken then, and not while a graph is captured: there pass detached
+    tensors and call combine_rows_backward."""
+    if torch.is_grad_enabled():
+        for name, t in (("rows", rows), ("w", w)):
+            if t is not None and t.requires_grad:
+                _no_capture(rows, name, "combine_rows_backward")
+                _need(out is None, "out: not with tensors that require a gradient")
+                return _CombineRows.apply(rows, routes["offsets"], routes["positions"], w, out_dtype, stream)
+    return _combine_rows(rows, routes, w, out_dtype, out, stream)
+
+
+def _combine_rows(rows, routes, w, out_dtype, out, stream):
+    _need(rows.dim() == 2, "rows: needs two dimensions")
+    dev = _device(rows)
+    positions, _, _ = _positions(routes, dev, False)
+    (T, K), (n, cols) = positions.shape, rows.shape
+    _int32(T | K | n | cols)
+    _check("rows", rows, dev, _ANY_FLOAT, (n, cols), pitched=True)
+    if w is not None:
+        _check("w", w, dev, _F32, (T, K))
+    out = _out(out, T, cols, rows.dtype if out_dtype is None else out_dtype, dev, stream)
+    _hold(stream, rows, positions, w, out)
+    _run("moe_combine_rows", dev, stream, T, K, n, cols, rows.data_ptr(), _pitch(rows), _FLOATS[rows.dtype],
+         positions.data_ptr(), _ptr(w), out.data_ptr(), _pitch(out), _FLOATS[out.dtype])
+    return out
+
+
+def combine_rows_backward(grad_out: torch.Tensor, rows: torch.Tensor, routes: dict, w=None, want_rows: bool = True,
+                          want_w: bool = True, zero_rest: bool = False, grad_rows=None, stream=None):
+    """moe_combine_rows_backward: (the gradient of rows, of their type, or into
+    grad_rows; that of w [T][K] fp32) for grad_out [T][cols], or None for one not
+    wanted. Rows behind the last route are left as they are (as allocated), or
+    zeros with zero_rest."""
+    _need(grad_out.dim() == 2 and rows.dim() == 2, "grad_out, rows: need two dimensions")
+    dev = _device(rows)
+    positions, taken, offsets = _positions(routes, dev, zero_rest)
+    (T, K), (n, cols) = positions.shape, rows.shape
+    _int32(T | K | n | cols)
+    _check("grad_out", grad_out, dev, _ANY_FLOAT, (T, cols), pitched=True)
+    _check("rows", rows, dev, _ANY_FLOAT, (n, cols), pitched=True)
+    if w is not None:
+        _check("w", w, dev, _F32, (T, K))
+    if grad_rows is not None:
+        _need(want_rows, "grad_rows: given, but not wanted")
+        _check("grad_rows", grad_rows, dev, (rows.dtype,), (n, cols), pitched=True)
+    elif want_rows:
+        grad_rows = _empty((n, cols), rows.dtype, dev, stream)
+    grad_w = _empty((T, K), torch.float32, dev, stream) if want_w else None
+    if not (want_rows or want_w):
+        return None, None
+    _hold(stream, grad_out, rows, positions, offsets, w, grad_rows)
+    _run("moe_combine_rows_backward", dev, stream, T, K, n, cols, grad_out.data_ptr(), _pitch(grad_out),
+         _FLOATS[grad_out.dtype], rows.data_ptr(), _pitch(rows), _FLOATS[rows.dtype], positions.data_ptr(), _ptr(w),
+         taken, _ptr(grad_rows), _pitch(grad_rows) if want_rows else cols, _ptr(grad_w))
+    return grad_rows, grad_w
+
+
+class _CombineRows(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, offsets, positions, w, out_dtype, stream):
+        ctx.save_for_backward(rows, offsets, positions, w)
+        return _combine_rows(rows, dict(offsets=offsets, positions=positions), w, out_dtype, None, stream)
+
+    @staticmethod
+    def backward(ctx, grad_out):
+        _once("combine_rows")
+        rows, offsets, positions, w = ctx.saved_tensors
+        _hold(torch.cuda.current_stream(rows.device), rows, offsets, positions, w)
+        grad_rows, grad_w = combine_rows_backward(
+            grad_out.contiguous(), rows, dict(offsets=offsets, positions=positions), w, ctx.needs_input_grad[0],
+            ctx.needs_input_grad[3], True)
+        return grad_rows, None, None, grad_w, None, None
 
 
 def balance_workspace_bytes(T: int, n_experts: int) -> int:

@@ -3,35 +3,18 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "api_checks.h"
 #include "balance.h"
 #include "fp8.h"
 #include "kernels.h"
 #include "moe.h"
 
+using namespace moe;
+
 namespace {
-
-constexpr int32_t kMaxRows = 1 << 28;
-constexpr int32_t kMaxWidth = 65536;
-constexpr int64_t kMaxPitch = int64_t{1} << 22;  // elements between rows
-constexpr int64_t kDescriptor = int64_t{1} << 31;  // bytes one buffer descriptor spans
-
-bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-int need(const void* p, size_t n) {
-  if (!p) return MOE_EINVAL;
-  return aligned(p, n) ? MOE_OK : MOE_EALIGN;
-}
-
-int type_ok(int32_t type) { return type == MOE_TYPE_BF16 || type == MOE_TYPE_F32 ? MOE_OK : MOE_EINVAL; }
 
 // The type of a product's out without MOE_SUM_F32.
 int32_t out_type_of(int32_t type) { return type >= 0 ? type & ~MOE_SUM_F32 : type; }
-
-#define MOE_TRY(expr)              \
-  do {                             \
-    const int rc_ = (expr);        \
-    if (rc_ != MOE_OK) return rc_; \
-  } while (0)
 
 int check_quant(int32_t rows, int32_t cols, int32_t wide, const void* x, int64_t ldx, int32_t type,
                 const uint8_t* codes, const float* scales) {

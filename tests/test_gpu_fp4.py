@@ -1,0 +1,472 @@
+"""The 4-bit rows and their products on the GPU against 64-bit definitions
+(tests/fp4_ref.py): group edges, ragged widths, few and many rows, empty
+experts, strides, gathers, NaN and infinities, streams, graphs."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from tests import fp4_ref as R
+
+pytestmark = pytest.mark.gpu
+B = pytest.importorskip("latent_mixture_experts_amd.binding")
+TYPES = [torch.bfloat16, torch.float32]
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def activations(rows, cols, g, dtype):
+    x = torch.randn((rows, cols), generator=g) * torch.exp(2 * torch.randn((rows, 1), generator=g))
+    return x.to(dtype)
+
+
+# ---- rows ------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols", [(1, 32), (1, 8192), (3, 96), (5, 128), (17, 160), (64, 288), (33, 4096),
+                                       (1000, 2080), (2500, 640)])
+def test_quantize(rows, cols, dtype):
+    x = activations(rows, cols, gen(rows + cols), dtype)
+    codes, scales = B.fp4_quantize(x.cuda())
+    ref, ref_s = R.quantize(x)
+    assert torch.equal(scales.cpu(), ref_s)
+    assert torch.equal(codes.cpu(), ref)
+    for out in TYPES:  # exact in both: two significant bits
+        assert torch.equal(B.fp4_dequantize(codes, scales, out).cpu().double(), R.values(ref, ref_s))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_quantize_special_values(dtype):
+    inf, nan = float("inf"), float("nan")
+    x = torch.zeros((12, 128))
+    x[0, 3] = 1.0                                  # one value, the rest zero
+    x[1] = torch.linspace(-7, 7, 128)
+    x[2, 5], x[2, 70], x[2, 127] = inf, nan, -inf  # three groups of four
+    x[3] = nan
+    x[4] = 2.0 ** -126
+    x[4, 64:] = 2.0 ** -133                        # bf16's smallest
+    x[5] = torch.finfo(dtype).max
+    x[5, 1] = -torch.finfo(dtype).max / 16
+    x[6] = -0.0
+    x[7, :32] = torch.tensor([.25, .75, 1.25, 1.75, 2.5, 3.5, 5., 6.] * 4) * 2.0 ** 5    # ties of the codes
+    x[7, 32:64] = -x[7, :32] * 2.0 ** -90
+    x[7, 64:] = 1.75
+    x[8, ::32] = torch.tensor([1.75, 1.7421875, 3.5, 3.484375])  # borders of the scale, in bf16
+    x[9, ::32] = torch.tensor([2.0 ** -124, 2.0 ** -125, 1.75 * 2.0 ** -126, 2.0 ** -126])  # and its bound
+    x[9, 1::32] = 2.0 ** -126
+    x[10] = 2.0 ** -149 if dtype == torch.float32 else 2.0 ** -133
+    x[11] = torch.finfo(dtype).max * torch.where(torch.arange(128) % 2 == 0, 1.0, -1.0)
+    x = x.to(dtype)
+    codes, scales = B.fp4_quantize(x.cuda())
+    ref, ref_s = R.quantize(x)
+    assert torch.equal(scales.cpu(), ref_s)
+    assert torch.equal(codes.cpu(), ref)
+    assert (scales[2].cpu() == torch.tensor([255, 1, 255, 255])).all() and (scales[3] == 255).all()
+    back = B.fp4_dequantize(codes, scales, torch.float32).cpu()
+    want = R.values(ref, ref_s)
+    # (the largest values round to twice the power of two that the type's largest lies below: infinite in fp32)
+    assert torch.equal(torch.isnan(back), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(back.double(), 0, 1e300, -1e300),
+                       torch.nan_to_num(want.float().double(), 0, 1e300, -1e300))
+
+
+def test_quantize_borders_of_every_exponent():
+    """Every bf16 value as the largest of a group and as a member under each larger power of two."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    x = torch.zeros((65536, 32), dtype=torch.bfloat16)
+    x[:, 0] = bits
+    x[:, 1] = bits * 0.5
+    x[:, 2] = -bits * 0.125
+    x[:, 3:11] = bits[:, None] * torch.tensor([.25, .375, .75, 1 / 16, 1 / 32, 1 / 64, -.0625, .875]).bfloat16()
+    codes, scales = B.fp4_quantize(x.cuda())
+    ref, ref_s = R.quantize(x)
+    assert torch.equal(scales.cpu(), ref_s) and torch.equal(codes.cpu(), ref)
+
+
+def test_quantize_strided_rows_and_given_outputs():
+    g = gen(5)
+    wide = activations(40, 1024, g, torch.bfloat16).cuda()
+    for cols in (256, 224):  # (with and without scales in words)
+        x = wide[:, 256:256 + cols]
+        ref, ref_s = R.quantize(x.cpu())
+        for shift in (0, 1):  # scales at any address
+            codes = torch.full((40, cols // 2), 9, dtype=torch.uint8, device="cuda")
+            hold = torch.full((40 * cols // 32 + 2,), 77, dtype=torch.uint8, device="cuda")
+            scales = hold[shift:shift + 40 * cols // 32].view(40, cols // 32)
+            B.fp4_quantize(x, codes, scales)
+            assert torch.equal(codes.cpu(), ref) and torch.equal(scales.cpu(), ref_s)
+            assert (hold[:shift] == 77).all() and (hold[shift + scales.numel():] == 77).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,inter", [(1, 32), (7, 96), (300, 512), (65, 4096), (1200, 1056)])
+def test_swiglu(rows, inter, dtype):
+    x = activations(rows, 2 * inter, gen(rows * inter), dtype)
+    codes, scales = B.fp4_swiglu(x.cuda())
+    v = x.double()
+    h = v[:, :inter] * torch.sigmoid(v[:, :inter]) * v[:, inter:]
+    # h in fp32: the exponential and the reciprocal to a step each, three products, two sums: 8 steps at most
+    slop = 8 * R.STEP32
+    m = h.abs().view(rows, -1, 32).amax(2)
+    lo, hi = (R.quantize(((1 + d) * m)[..., None].expand(-1, -1, 32).reshape(rows, -1))[1] for d in (-slop, slop))
+    s = scales.cpu()
+    assert bool(((s >= lo) & (s <= hi)).all())
+    step = torch.exp2(s.double() - 127).repeat_interleave(32, 1)
+    off = (R.values(codes.cpu(), s) - h).abs()
+    assert bool((off <= R.half_step(h / step * (1 + slop)) * step + h.abs() * slop + 1e-45).all())
+
+
+def test_swiglu_special_values():
+    x = torch.zeros((4, 128))
+    x[0, :64] = torch.linspace(-120, 120, 64)     # gates over the exponential's range
+    x[0, 64:] = 1.0
+    x[1, :64], x[1, 64:] = float("inf"), 2.0      # silu(inf) = inf: the group is NaN
+    x[2, 3], x[2, 64 + 3] = float("nan"), 1.0
+    x[2, 40], x[2, 64 + 40] = 3.0, -2.0
+    x[3, :64], x[3, 64:] = -200.0, 1e30           # silu is 0 in fp32
+    codes, scales = B.fp4_swiglu(x.cuda())
+    assert scales.cpu()[1].tolist() == [255, 255] and scales.cpu()[2, 0] == 255 and scales.cpu()[2, 1] != 255
+    assert (codes.cpu()[1] == 0).all() and ((codes.cpu()[3] & 0x77) == 0).all()
+    v = x[0].double()
+    h = v[:64] * torch.sigmoid(v[:64])
+    step = torch.exp2(scales.cpu()[0].double() - 127).repeat_interleave(32)
+    assert bool(((R.values(codes.cpu()[0], scales.cpu()[0]) - h).abs() <= R.half_step(h / step) * step * (1 + 1e-6)).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_dequantize_every_byte_and_scale(dtype):
+    codes = torch.arange(256, dtype=torch.int32).to(torch.uint8).view(16, 16).repeat_interleave(256, 0)
+    scales = torch.arange(256, dtype=torch.int32).to(torch.uint8).repeat(16)[:, None]
+    want = R.values(codes, scales)
+    got = B.fp4_dequantize(codes.cuda(), scales.cuda(), dtype).cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    fine = ~torch.isnan(want)  # (2^128 and more: infinite)
+    assert torch.equal(got[fine].float(), want[fine].to(dtype).float())
+    wide = torch.full((4096, 37), 5.0, dtype=dtype, device="cuda")  # rows at an odd pitch, off 16 bytes
+    B.fp4_dequantize(codes.cuda(), scales.cuda(), out=wide[:, 3:35])
+    assert torch.equal(wide[:, 3:35].cpu()[fine].float(), want[fine].to(dtype).float())
+    assert (wide[:, :3] == 5).all() and (wide[:, 35:] == 5).all()
+
+
+def test_rows_of_more_than_one_launch():
+    """More than 2^24 rows: several launches of the quantisation and back."""
+    rows = (1 << 24) + 77
+    x = torch.empty((rows, 32), dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    codes, scales = B.fp4_quantize(x)
+    back = B.fp4_dequantize(codes, scales)
+    at = torch.cat([torch.arange(64), torch.arange((1 << 24) - 64, rows)]).cuda()
+    ref, ref_s = R.quantize(x[at].cpu())
+    assert torch.equal(codes[at].cpu(), ref) and torch.equal(scales[at].cpu(), ref_s)
+    assert torch.equal(back[at].cpu().double(), R.values(ref, ref_s))
+
+
+# ---- products ----------------------------------------------------------------
+
+def operands(T, N, K, g, experts=None):
+    lead = () if experts is None else (experts,)
+    return (R.random_codes((T, K // 2), g), R.random_scales((T, K // 32), g),
+            R.random_codes((*lead, N, K // 2), g), R.random_scales((*lead, N, K // 32), g))
+
+
+def check(got, x, xs, w, ws, dtype, what=""):
+    x, xs, w, ws = (t.cuda() for t in (x, xs, w, ws))
+    out, mag = R.product(x, xs, w, ws)
+    err = (got.double() - out).abs()
+    bound = R.product_bound(out, mag, 2 * x.shape[1], dtype)
+    assert bool((err <= bound).all()), (what, float((err / bound).max()))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,N,K", [
+    (1, 1, 32), (1, 16, 64), (1, 4096, 8192), (2, 33, 96), (3, 257, 160), (8, 64, 480), (15, 100, 512), (16, 130, 544),
+    (17, 96, 1024), (31, 48, 2080), (32, 512, 256), (33, 8192, 4096), (48, 200, 1536), (63, 65, 4128), (64, 64, 128),
+    (65, 129, 640), (100, 1000, 992), (127, 255, 1280), (128, 256, 512), (129, 257, 288), (200, 2050, 768),
+    (256, 4096, 1024), (257, 300, 2016), (500, 513, 1152), (1000, 1024, 736), (2048, 2048, 512), (4100, 260, 352),
+    (4096, 4096, 1024)])
+def test_linear(T, N, K, dtype):
+    ops = operands(T, N, K, gen(T * 7 + N * 3 + K))
+    check(B.fp4_linear(*(t.cuda() for t in ops), dtype), *ops, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T", [1, 5, 16, 40, 300])
+def test_linear_wide_scales(T, dtype):
+    """Scales over 2^-60 .. 2^60: sums whose terms differ by far more than fp32 holds, still by fp32 additions."""
+    g = gen(T)
+    x, w = R.random_codes((T, 640), g), R.random_codes((200, 640), g)
+    xs, ws = R.random_scales((T, 40), g, 67, 187), R.random_scales((200, 40), g, 97, 157)
+    check(B.fp4_linear(*(t.cuda() for t in (x, xs, w, ws)), dtype), x, xs, w, ws, dtype)
+
+
+@pytest.mark.parametrize("T", [3, 100])
+def test_linear_small_and_large_results(T):
+    g = gen(T)
+    x, w = R.random_codes((T, 256), g), R.random_codes((70, 256), g)
+    for lo, hi in ((1, 30), (60, 80)):  # results below fp32's normal numbers, or none at all
+        xs, ws = R.random_scales((T, 16), g, lo, hi), R.random_scales((70, 16), g, 30, 60)
+        check(B.fp4_linear(*(t.cuda() for t in (x, xs, w, ws)), torch.float32), x, xs, w, ws, torch.float32)
+    xs, ws = torch.full((T, 16), 254, dtype=torch.uint8), torch.full((70, 16), 254, dtype=torch.uint8)
+    out, _ = R.product(x, xs, w, ws)
+    got = B.fp4_linear(*(t.cuda() for t in (x, xs, w, ws)), torch.float32).cpu()
+    big = out != 0
+    assert bool((~torch.isfinite(got[big])).all())  # (2^254 and more; NaN where infinities of both signs meet)
+
+
+@pytest.mark.parametrize("T", [4, 40, 300])
+def test_nan_scales_stay_in_their_row_and_column(T):
+    g = gen(T)
+    x, xs, w, ws = operands(T, 150, 1024, g)
+    want = R.product(x, xs, w, ws)[0]
+    xs[2, 5] = 255
+    ws[100, 31] = 255
+    got = B.fp4_linear(*(t.cuda() for t in (x, xs, w, ws)), torch.float32).cpu()
+    nan = torch.isnan(got)
+    assert nan[2].all() and nan[:, 100].all()
+    keep = torch.ones_like(nan)
+    keep[2], keep[:, 100] = False, False
+    assert not nan[keep].any()
+    assert torch.allclose(got[keep].double(), want[keep], rtol=1e-3, atol=float(want.abs().max()) * 1e-5)
+
+
+@pytest.mark.parametrize("T,K", [(5, 256), (33, 512), (70, 416), (300, 1024)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_linear_strides_and_alignments(T, K, dtype):
+    """x rows at a pitch, out rows at an odd pitch off 16 bytes, scales at odd addresses."""
+    g = gen(T + K)
+    x, xs, w, ws = operands(T, 96, K, g)
+    wide = torch.zeros((T, K // 2 + 48), dtype=torch.uint8, device="cuda")
+    wide[:, 16:16 + K // 2] = x.cuda()
+
+    def off(t, by):
+        hold = torch.zeros(t.numel() + 16, dtype=torch.uint8, device="cuda")
+        hold[by:by + t.numel()] = t.cuda().flatten()
+        return hold[by:by + t.numel()].view(t.shape)
+
+    for by in (0, 1, 4):
+        out = torch.full((T, 101), 3.0, dtype=dtype, device="cuda")
+        B.fp4_linear(wide[:, 16:16 + K // 2], off(xs, by), w.cuda(), off(ws, by and 16 - by), out=out[:, 1:97])
+        check(out[:, 1:97], x, xs, w, ws, dtype, by)
+        assert (out[:, 0] == 3).all() and (out[:, 97:] == 3).all()
+
+
+def test_linear_refusals():
+    x, xs, w, ws = (t.cuda() for t in operands(4, 64, 128, gen(1)))
+    for bad in (lambda: B.fp4_linear(x, xs[:, :3], w, ws), lambda: B.fp4_linear(x, xs, w[:, :32], ws),
+                lambda: B.fp4_linear(x, xs, w, ws[:60]), lambda: B.fp4_linear(x.int(), xs, w, ws),
+                lambda: B.fp4_linear(x, xs, w, ws, torch.float16), lambda: B.fp4_linear(x.cpu(), xs, w, ws),
+                lambda: B.fp4_linear(x, xs.cpu(), w, ws), lambda: B.fp4_linear(x[0], xs, w, ws),
+                lambda: B.fp4_linear(x, xs, w, ws, out=torch.empty((4, 63), device="cuda")),
+                lambda: B.fp4_quantize(torch.zeros((2, 48), device="cuda")),
+                lambda: B.fp4_quantize(torch.zeros((2, 64), device="cuda", dtype=torch.float16)),
+                lambda: B.fp4_quantize(torch.zeros((64, 64), device="cuda").t()[:, ::2]),
+                lambda: B.fp4_swiglu(torch.zeros((2, 96), device="cuda")),
+                lambda: B.fp4_dequantize(x, xs[:, :3]),
+                lambda: B.fp4_grouped(x, xs, torch.zeros(2, dtype=torch.int32, device="cuda"), w[None], ws[None, :3])):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(B.MoeError) as e:  # rows of x off 16 bytes
+        B.fp4_linear(torch.zeros((4, 72), dtype=torch.uint8, device="cuda")[:, :64], xs, w, ws)
+    assert e.value.status == B.MOE_EALIGN
+    assert B.fp4_linear(x[:0], xs[:0], w, ws).shape == (0, 64)
+    assert B.fp4_quantize(torch.empty((0, 64), device="cuda"))[0].shape == (0, 32)
+
+
+def test_linear_takes_e8m0_scales_and_the_same_bits_every_time():
+    ops = [t.cuda() for t in operands(700, 900, 1024, gen(9))]
+    a = B.fp4_linear(*ops, torch.float32)
+    b = B.fp4_linear(ops[0], ops[1].view(torch.float8_e8m0fnu), ops[2], ops[3].view(torch.float8_e8m0fnu), torch.float32)
+    assert torch.equal(a, b)
+
+
+# ---- per expert ----------------------------------------------------------------
+
+def grouping(counts):
+    return torch.tensor([0] + list(torch.tensor(counts).cumsum(0)), dtype=torch.int32)
+
+
+def check_grouped(got, x, xs, off, w, ws, dtype, rows=None):
+    for e in range(w.shape[0]):
+        a, b = int(off[e]), int(off[e + 1])
+        if b > a:
+            at = torch.arange(a, b) if rows is None else rows[a:b]
+            check(got[a:b], x[at], xs[at], w[e], ws[e], dtype, e)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("counts,N,K", [
+    ([3], 64, 64), ([0, 1, 0, 2, 0], 40, 96), ([16, 17, 1, 0, 33], 130, 512), ([1] * 64, 256, 1024),
+    ([0] * 100 + [5] + [0] * 155, 72, 160), ([2, 0, 300, 7, 64], 200, 288), ([128] * 8, 256, 512), ([40, 90, 1, 200] * 4, 300, 544),
+    ([700, 0, 3], 513, 256), ([1, 2, 3, 0] * 64, 128, 256), ([130] * 40, 512, 128), ([17] * 200, 96, 1024)])
+def test_grouped(counts, N, K, dtype):
+    rows = sum(counts)
+    x, xs, w, ws = operands(rows, N, K, gen(rows + N + K), len(counts))
+    off = grouping(counts)
+    got = B.fp4_grouped(x.cuda(), xs.cuda(), off.cuda(), w.cuda(), ws.cuda(), dtype)
+    check_grouped(got, x, xs, off, w, ws, dtype)
+
+
+@pytest.mark.parametrize("T,E,K_,N,K", [(1, 16, 8, 100, 512), (9, 8, 3, 64, 96), (61, 32, 4, 200, 1024), (300, 8, 2, 256, 288),
+                                       (1000, 4, 2, 130, 512)])
+def test_grouped_gathers_tokens(T, E, K_, N, K):
+    g = gen(T)
+    x, xs, w, ws = operands(T, N, K, g, E)
+    ids = torch.stack([torch.randperm(E, generator=g)[:K_] for _ in range(T)]).to(torch.int32)
+    routes = B.sort_routes(ids.cuda(), E)
+    got = B.fp4_grouped(x.cuda(), xs.cuda(), routes["offsets"], w.cuda(), ws.cuda(), torch.float32,
+                        row_index=routes["sorted"], index_div=K_)
+    check_grouped(got, x, xs, routes["offsets"].cpu(), w, ws, torch.float32, routes["sorted"].cpu().long() // K_)
+
+
+@pytest.mark.parametrize("rows", [30, 400])
+def test_grouped_leaves_other_rows(rows):
+    g = gen(rows)
+    x, xs, w, ws = operands(rows, 72, 256, g, 3)
+    off = torch.tensor([4, 9, 9, rows - 5], dtype=torch.int32)
+    out = torch.full((rows, 72), -7.0, device="cuda")
+    B.fp4_grouped(x.cuda(), xs.cuda(), off.cuda(), w.cuda(), ws.cuda(), out=out)
+    check_grouped(out, x, xs, off, w, ws, torch.float32)
+    assert (out[:4] == -7).all() and (out[rows - 5:] == -7).all()
+
+
+@pytest.mark.parametrize("rows", [20, 300])
+def test_grouped_bad_lists_stay_in_bounds(rows):
+    """Offsets that decrease or leave the rows, indices outside x: nothing outside the buffers is touched."""
+    g = gen(rows)
+    x, xs, w, ws = (t.cuda() for t in operands(rows, 64, 128, g, 4))
+    hold = torch.full((rows + 200, 64), -7.0, device="cuda")
+    out = hold[100:100 + rows]
+    for off in ([0, rows + 50, 3, -9, rows], [-5, 2, 1 << 30, 7, 9], [rows, 0, rows, 0, rows]):
+        B.fp4_grouped(x, xs, torch.tensor(off, dtype=torch.int32).cuda(), w, ws, out=out)
+    idx = torch.randint(-(1 << 31), (1 << 31) - 1, (rows,), generator=g).to(torch.int32)
+    B.fp4_grouped(x, xs, torch.tensor([0, 5, 5, 10, rows], dtype=torch.int32).cuda(), w, ws, out=out, row_index=idx.cuda())
+    assert (hold[:100] == -7).all() and (hold[100 + rows:] == -7).all()
+    clamped = idx.long().clamp(0, rows - 1)
+    check_grouped(out, x.cpu(), xs.cpu(), [0, 5, 5, 10, rows], w.cpu(), ws.cpu(), torch.float32, clamped)
+
+
+def test_grouped_offsets_past_32_bits():
+    """Weights of more than 4 GiB: the last expert's."""
+    E, N, K = 9, 32768, 32768
+    g = torch.Generator("cuda").manual_seed(3)
+    w = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    ws = torch.randint(117, 133, (E, N, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+    assert w.numel() > 1 << 32
+    for rows in (3, 40):
+        x = torch.randint(0, 256, (rows, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+        xs = torch.randint(117, 133, (rows, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+        off = torch.tensor([0, 1] + [1] * (E - 2) + [rows], dtype=torch.int32, device="cuda")
+        got = B.fp4_grouped(x, xs, off, w, ws, torch.float32)
+        for e, a, b in ((0, 0, 1), (E - 1, 1, rows)):
+            for n in (0, 5000, N - 300):
+                check(got[a:b, n:n + 300], x[a:b], xs[a:b], w[e, n:n + 300], ws[e, n:n + 300], torch.float32, (rows, e, n))
+
+
+def test_grouped_on_the_layers_weights():
+    """The layer's own w13 bytes of a reduced configuration."""
+    from latent_mixture_experts_amd import synth
+
+    dims = dict(hidden=512, latent=384, inter=256, n_experts=24, top_k=6)
+    ex = synth.all_expert_bytes(dims, 7, device="cuda")
+    E, N, K = 24, 512, 384
+    w, ws = ex["w13_codes"].view(torch.uint8).view(E, N, K // 2), ex["w13_scales"].view(torch.uint8).view(E, N, K // 32)
+    x = activations(50, K, gen(2), torch.bfloat16).cuda()
+    codes, scales = B.fp4_quantize(x)
+    counts = [3, 0, 9, 2] * 3 + [1] * 8 + [0] * 4
+    off = grouping(counts)
+    got = B.fp4_grouped(codes, scales, off.cuda(), w, ws, torch.float32)
+    check_grouped(got, codes.cpu(), scales.cpu(), off, w.cpu(), ws.cpu(), torch.float32)
+
+
+# ---- streams and graphs ----------------------------------------------------------
+
+def test_other_stream_and_dropped_tensors():
+    ops = operands(40, 512, 1024, gen(3))
+    x = activations(40, 1024, gen(4), torch.bfloat16)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    dev = [t.cuda() for t in ops]
+    xd = x.cuda()
+    torch.cuda.current_stream().synchronize()
+    codes, scales = B.fp4_quantize(xd, stream=side)
+    out = B.fp4_linear(*dev, torch.float32, stream=side)
+    back = B.fp4_dequantize(codes, scales, stream=side)
+    del dev, xd
+    junk = [torch.full((1 << 20,), 3, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    side.synchronize()
+    check(out, *ops, torch.float32)
+    ref, ref_s = R.quantize(x)
+    assert torch.equal(back.cpu().double(), R.values(ref, ref_s))
+    del junk
+
+
+def test_captured_and_replayed():
+    """quantize -> grouped -> swiglu -> grouped -> combine in a graph, replayed on new inputs with eager work between."""
+    T, E, K_, L, I = 24, 8, 4, 256, 128
+    g = gen(8)
+    x = activations(T, L, g, torch.bfloat16).cuda()
+    w13, s13 = R.random_codes((E, 2 * I, L // 2), g).cuda(), R.random_scales((E, 2 * I, L // 32), g, 117, 119).cuda()
+    w2, s2 = R.random_codes((E, L, I // 2), g).cuda(), R.random_scales((E, L, I // 32), g, 117, 119).cuda()
+    ids = torch.stack([torch.randperm(E, generator=g)[:K_] for _ in range(T)]).to(torch.int32).cuda()
+    w = torch.rand((T, K_), generator=g).cuda()
+
+    def ffn():
+        routes = B.sort_routes(ids, E)
+        c, s = B.fp4_quantize(x)
+        gu = B.fp4_grouped(c, s, routes["offsets"], w13, s13, torch.float32, row_index=routes["sorted"], index_div=K_)
+        c, s = B.fp4_swiglu(gu)
+        return B.combine_rows(B.fp4_grouped(c, s, routes["offsets"], w2, s2, torch.float32), routes, w)
+
+    ffn()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = ffn()
+    for i in range(4):
+        x.copy_(activations(T, L, gen(50 + i), torch.bfloat16))
+        ids.copy_(torch.stack([torch.randperm(E, generator=g)[:K_] for _ in range(T)]))
+        w.copy_(torch.rand((T, K_), generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ffn())
+
+
+def test_layer_in_four_bits():
+    """route -> quantize -> pooler -> sort -> gate/up -> swiglu -> down -> weighted sum -> unpooler, each product
+    and the sum against 64 bits on the GPU's own intermediates."""
+    from latent_mixture_experts_amd import synth
+
+    dims = dict(hidden=512, latent=256, inter=128, n_experts=16, top_k=4)
+    T, E, K_, H, L, I = 37, 16, 4, 512, 256, 128
+    lay = synth.make_layer(dims, T, seed=5)
+    ex = synth.all_expert_bytes(dims, 5, device="cuda")
+    g = gen(6)
+    x = torch.from_numpy(lay.x).view(torch.int16).cuda()
+    d = B.make_dims(dims)
+    r = B.route(d, x, torch.from_numpy(lay.router).cuda(), B.alloc_workspace(d, T))
+    routes = B.sort_routes(r["ids"], E)
+    assert torch.equal(routes["offsets"], r["offsets"]) and torch.equal(routes["sorted"], r["sorted"])
+
+    pool, unpool = B.fp4_quantize(torch.randn((L, H), generator=g).cuda()), B.fp4_quantize(torch.randn((H, L), generator=g).cuda())
+    xq = B.fp4_quantize(x.view(torch.bfloat16))
+    lat = B.fp4_linear(*xq, *pool)
+    check(lat, *xq, *pool, torch.bfloat16)
+    lq = B.fp4_quantize(lat)
+    w13, s13 = ex["w13_codes"].view(torch.uint8).view(E, 2 * I, L // 2), ex["w13_scales"].view(torch.uint8).view(E, 2 * I, L // 32)
+    w2, s2 = ex["w2_codes"].view(torch.uint8).view(E, L, I // 2), ex["w2_scales"].view(torch.uint8).view(E, L, I // 32)
+    off, token = routes["offsets"].cpu(), routes["sorted"].cpu().long() // K_
+    gu = B.fp4_grouped(*lq, routes["offsets"], w13, s13, row_index=routes["sorted"], index_div=K_)
+    check_grouped(gu, lq[0].cpu(), lq[1].cpu(), off, w13.cpu(), s13.cpu(), torch.bfloat16, token)
+    hq = B.fp4_swiglu(gu)
+    rows = B.fp4_grouped(*hq, routes["offsets"], w2, s2, torch.float32)
+    check_grouped(rows, hq[0].cpu(), hq[1].cpu(), off, w2.cpu(), s2.cpu(), torch.float32)
+    y = B.combine_rows(rows, routes, r["w"], torch.bfloat16)
+    terms = r["w"].double()[:, :, None] * rows.double()[routes["positions"].long()]
+    want = terms.sum(1)
+    # a rounding of each product and sum (2 K_ of half a step), then half a step of bf16
+    bound = terms.abs().sum(1) * (K_ + 1) * 2.0 ** -23 + want.abs() * 2.0 ** -8 * (1 + 2.0 ** -8) + 1e-37
+    assert bool(((y.double() - want).abs() <= bound).all())
+    yq = B.fp4_quantize(y)
+    out = B.fp4_linear(*yq, *unpool)
+    check(out, *yq, *unpool, torch.bfloat16)
