@@ -50,6 +50,7 @@ struct Fp4Gemm {
   int rows, x_rows, experts, N, K, index_div;
   bool f32;       // out fp32, else bf16
   bool out_vec;   // out rows take four-value stores (base and pitch aligned)
+  bool out_vec8;  // and eight-value ones (bf16)
   bool scale_vec; // scale rows start at multiples of 16 bytes, in x and w
 };
 hipError_t launch_fp4_gemm(const Fp4Gemm& g, hipStream_t st);

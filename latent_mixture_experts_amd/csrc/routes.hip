@@ -21,27 +21,56 @@ namespace moe {
 namespace {
 
 // ---- sort ------------------------------------------------------------------
-// A stable counting sort: within an expert routes ascend. Routes to no expert
-// here are one more bucket behind the last, so that every entry of sorted is
-// written. Lanes with the same bucket find each other with nine ballots, a
-// lane's rank among them is a popcount.
-constexpr int kSortWaves = 16;
-constexpr int kBuckets = 257;
+// A stable counting sort: within an expert routes ascend. Lanes with the same
+// expert find each other with eight ballots, a lane's rank among them is a
+// popcount. Routes to no expert here take no place; what lies behind the last
+// place becomes -1.
+//
+// Up to kOneGroup routes: one workgroup, each wavefront a run of routes, walked
+// twice (counts, places). More: chunks of kChunk routes, counted by a workgroup
+// each; a second launch gives every chunk's places, its workgroups each adding
+// up the chunks before their own (up to kFewChunks, where that is little), or
+// after a launch that turns the counts into places first.
+constexpr int kSortWaves = 16, kRun = 128, kChunk = kSortWaves * kRun;
+constexpr int kOneGroup = 3 * kChunk, kFewChunks = 64, kExperts = 256;
 
-__device__ __forceinline__ int bucket_of(const SortRoutes& s, int r) {
+__device__ __forceinline__ int expert_of(const SortRoutes& s, int64_t r, int64_t end) {
+  if (r >= end) return -1;
   const int64_t e = static_cast<int64_t>(s.ids[r]) - s.first;
-  return e >= 0 && e < s.E ? static_cast<int>(e) : s.E;
+  return e >= 0 && e < s.E ? static_cast<int>(e) : -1;
 }
 
-// The lanes in range with this lane's bucket.
-__device__ __forceinline__ uint64_t same_bucket(int e, bool valid) {
-  const uint64_t top = __ballot(valid && e == 256);
-  const uint64_t low = same_id_mask(e & 255, valid && e != 256);
-  return e == 256 ? top : low;
+// Adds the routes of [begin, end) to this wavefront's counts.
+__device__ __forceinline__ void count_routes(const SortRoutes& s, int64_t begin, int64_t end, int* count) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t b = begin; b < end; b += 64) {
+    const int e = expert_of(s, b + lane, end);
+    const uint64_t same = same_id_mask(e, e >= 0);
+    if (e >= 0 && (63 - __clzll(static_cast<long long>(same))) == lane) count[e] += __popcll(same);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // (another lane adds to it next time)
+  }
+}
+// Gives them their places, from each expert's next one.
+__device__ __forceinline__ void place_routes(const SortRoutes& s, int64_t begin, int64_t end, int* next) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t b = begin; b < end; b += 64) {
+    const int64_t r = b + lane;
+    const int e = expert_of(s, r, end);
+    const uint64_t same = same_id_mask(e, e >= 0);
+    int at = -1;
+    if (e >= 0) {
+      at = next[e] + __popcll(same & ((1ull << lane) - 1ull));
+      s.sorted[at] = static_cast<int32_t>(r);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // (every lane has read before one adds)
+      if ((63 - __clzll(static_cast<long long>(same))) == lane) next[e] += __popcll(same);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (r < end) s.positions[r] = at;
+  }
 }
 
-// Exclusive scan over the values of threads 0..256 (all 1024 call).
-__device__ int scan_buckets(int v, int* sums) {
+// Exclusive scan over the values of threads 0..255 (all 1024 call), and their sum.
+__device__ int scan_experts(int v, int* sums, int* total) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int incl = v;
 #pragma unroll
@@ -49,56 +78,139 @@ __device__ int scan_buckets(int v, int* sums) {
     const int o = __shfl_up(incl, d, 64);
     if (lane >= d) incl += o;
   }
-  if (lane == 63) sums[wave] = incl;
+  if (lane == 63 && wave < 4) sums[wave] = incl;
   __syncthreads();
   int base = 0;
-  for (int w = 0; w < wave && w < 5; ++w) base += sums[w];
+  for (int w = 0; w < 4; ++w) base += w < wave ? sums[w] : 0;
+  *total = sums[0] + sums[1] + sums[2] + sums[3];
   __syncthreads();
   return base + incl - v;
 }
 
-__global__ __launch_bounds__(1024) void sort_routes_kernel(SortRoutes s) {
-  __shared__ int hist[kSortWaves][kBuckets];
-  __shared__ int sums[kSortWaves];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int i = tid; i < kSortWaves * kBuckets; i += 1024) (&hist[0][0])[i] = 0;
+// hist[w][e], counts of wavefront w: each becomes its first place, base + those
+// of the wavefronts before. Threads below E.
+__device__ __forceinline__ void places_of_waves(int (*hist)[kExperts], int e, int base) {
+  for (int w = 0; w < kSortWaves; ++w) {
+    const int c = hist[w][e];
+    hist[w][e] = base;
+    base += c;
+  }
+}
+
+__global__ __launch_bounds__(1024) void sort_one_kernel(SortRoutes s) {
+  __shared__ int hist[kSortWaves][kExperts];
+  __shared__ int sums[4];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  for (int i = tid; i < kSortWaves * kExperts; i += 1024) (&hist[0][0])[i] = 0;
   __syncthreads();
   const int seg = ((s.R + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
-  const int64_t begin = static_cast<int64_t>(wave) * seg;
-  const int64_t end = begin + seg < s.R ? begin + seg : s.R;
-  for (int64_t b = begin; b < end; b += 64) {
-    const int64_t r = b + lane;
-    const bool valid = r < end;
-    const int e = valid ? bucket_of(s, static_cast<int>(r)) : 0;
-    const uint64_t same = same_bucket(e, valid);
-    if (valid && (63 - __clzll(static_cast<long long>(same))) == lane) hist[wave][e] += __popcll(same);
-  }
+  const int begin = min(wave * seg, s.R), end = min(begin + seg, s.R);
+  count_routes(s, begin, end, hist[wave]);
   __syncthreads();
-  int total = 0;
-  if (tid <= s.E)
-    for (int w = 0; w < kSortWaves; ++w) {
-      const int c = hist[w][tid];
-      hist[w][tid] = total;
-      total += c;
-    }
-  const int off = scan_buckets(tid <= s.E ? total : 0, sums);
-  if (tid <= s.E) {
+  int total = 0, all;
+  if (tid < s.E)
+    for (int w = 0; w < kSortWaves; ++w) total += hist[w][tid];
+  const int off = scan_experts(tid < s.E ? total : 0, sums, &all);
+  if (tid < s.E) {
     s.offsets[tid] = off;
-    for (int w = 0; w < kSortWaves; ++w) hist[w][tid] += off;
+    places_of_waves(hist, tid, off);
+  }
+  if (tid == 0) s.offsets[s.E] = all;
+  __syncthreads();
+  place_routes(s, begin, end, hist[wave]);
+  for (int i = all + tid; i < s.R; i += 1024) s.sorted[i] = -1;
+}
+
+// counts[c][e]: routes of chunk c to expert e
+__global__ __launch_bounds__(1024) void sort_count_kernel(SortRoutes s) {
+  __shared__ int hist[kSortWaves][kExperts];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  for (int i = tid; i < kSortWaves * kExperts; i += 1024) (&hist[0][0])[i] = 0;
+  __syncthreads();
+  const int64_t begin = static_cast<int64_t>(blockIdx.x) * kChunk + wave * kRun;
+  count_routes(s, begin, begin + kRun < s.R ? begin + kRun : s.R, hist[wave]);
+  __syncthreads();
+  if (tid < s.E) {
+    int total = 0;
+    for (int w = 0; w < kSortWaves; ++w) total += hist[w][tid];
+    s.counts[static_cast<size_t>(blockIdx.x) * kExperts + tid] = total;
+  }
+}
+
+// Many chunks: counts[c][e] becomes the number of e's routes in the chunks
+// before c; counts[G][e] their sum. A workgroup takes 16 experts, its threads 64
+// runs of chunks of each.
+__global__ __launch_bounds__(1024) void sort_scan_kernel(SortRoutes s, int G) {
+  __shared__ int sums[64][16];
+  const int e = static_cast<int>(blockIdx.x) * 16 + (threadIdx.x & 15), run = threadIdx.x >> 4;
+  const int per = (G + 63) / 64, c0 = min(run * per, G), c1 = min(c0 + per, G);
+  int total = 0;
+  if (e < s.E)
+    for (int c = c0; c < c1; ++c) total += s.counts[static_cast<size_t>(c) * kExperts + e];
+  sums[run][threadIdx.x & 15] = total;
+  __syncthreads();
+  int before = 0;
+  for (int i = 0; i < run; ++i) before += sums[i][threadIdx.x & 15];
+  if (e < s.E) {
+    for (int c = c0; c < c1; ++c) {
+      int* at = s.counts + static_cast<size_t>(c) * kExperts + e;
+      const int n = *at;
+      *at = before;
+      before += n;
+    }
+    if (run == 63) s.counts[static_cast<size_t>(G) * kExperts + e] = before;
+  }
+}
+
+// SCANNED: counts as sort_scan_kernel leaves them, else as counted.
+template <bool SCANNED>
+__global__ __launch_bounds__(1024) void sort_place_kernel(SortRoutes s, int G) {
+  __shared__ int hist[kSortWaves][kExperts];
+  __shared__ int sums[4];
+  __shared__ int part[2][4][kExperts];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int chunk = static_cast<int>(blockIdx.x);
+  for (int i = tid; i < kSortWaves * kExperts; i += 1024) (&hist[0][0])[i] = 0;
+  if constexpr (!SCANNED) {  // four threads to an expert
+    const int e = tid & 255, q = tid >> 8;
+    int before = 0, total = 0;
+    if (e < s.E) {
+#pragma unroll 8
+      for (int c = q; c < G; c += 4) {
+        const int n = s.counts[static_cast<size_t>(c) * kExperts + e];
+        total += n;
+        before += c < chunk ? n : 0;
+      }
+    }
+    part[0][q][e] = before;
+    part[1][q][e] = total;
   }
   __syncthreads();
-  for (int64_t b = begin; b < end; b += 64) {
-    const int64_t r = b + lane;
-    const bool valid = r < end;
-    const int e = valid ? bucket_of(s, static_cast<int>(r)) : 0;
-    const uint64_t same = same_bucket(e, valid);
-    if (valid) {
-      const int at = hist[wave][e] + __popcll(same & ((1ull << lane) - 1ull));
-      s.sorted[at] = e < s.E ? static_cast<int32_t>(r) : -1;
-      s.positions[r] = e < s.E ? at : -1;
-      if ((63 - __clzll(static_cast<long long>(same))) == lane) hist[wave][e] += __popcll(same);
+  const int64_t begin = static_cast<int64_t>(chunk) * kChunk + wave * kRun;
+  const int64_t end = begin + kRun < s.R ? begin + kRun : s.R;
+  count_routes(s, begin, end, hist[wave]);
+  __syncthreads();
+  int before = 0, total = 0, all;
+  if (tid < s.E) {
+    if constexpr (SCANNED) {
+      before = s.counts[static_cast<size_t>(chunk) * kExperts + tid];
+      total = s.counts[static_cast<size_t>(G) * kExperts + tid];
+    } else {
+      before = part[0][0][tid] + part[0][1][tid] + part[0][2][tid] + part[0][3][tid];
+      total = part[1][0][tid] + part[1][1][tid] + part[1][2][tid] + part[1][3][tid];
     }
   }
+  const int off = scan_experts(total, sums, &all);
+  if (tid < s.E) {
+    places_of_waves(hist, tid, off + before);
+    if (chunk == 0) s.offsets[tid] = off;
+  }
+  if (chunk == 0 && tid == 0) s.offsets[s.E] = all;
+  __syncthreads();
+  place_routes(s, begin, end, hist[wave]);
+  const int64_t stop = static_cast<int64_t>(chunk + 1) * kChunk < s.R ? static_cast<int64_t>(chunk + 1) * kChunk : s.R;
+  for (int64_t i = static_cast<int64_t>(chunk) * kChunk + tid; i < stop; i += 1024)
+    if (i >= all) s.sorted[i] = -1;
 }
 
 // ---- rows ------------------------------------------------------------------
@@ -263,10 +375,24 @@ dim3 token_grid(int T) { return dim3(static_cast<unsigned>(T < 1 ? 1 : T < (1 <<
 
 }  // namespace
 
-size_t sort_workspace(int, int) { return 0; }
+size_t sort_workspace(int R, int) {
+  if (R <= kOneGroup) return 0;
+  return static_cast<size_t>((R + kChunk - 1) / kChunk + 1) * kExperts * sizeof(int32_t);
+}
 
 hipError_t launch_sort_routes(const SortRoutes& s, hipStream_t st) {
-  MOE_LAUNCH((sort_routes_kernel), dim3(1), dim3(1024), 0, st, s);
+  if (s.R <= kOneGroup) {
+    MOE_LAUNCH((sort_one_kernel), dim3(1), dim3(1024), 0, st, s);
+    return hipGetLastError();
+  }
+  const int G = (s.R + kChunk - 1) / kChunk;
+  MOE_LAUNCH((sort_count_kernel), dim3(G), dim3(1024), 0, st, s);
+  if (G <= kFewChunks) {
+    MOE_LAUNCH((sort_place_kernel<false>), dim3(G), dim3(1024), 0, st, s, G);
+  } else {
+    MOE_LAUNCH((sort_scan_kernel), dim3((s.E + 15) / 16), dim3(1024), 0, st, s, G);
+    MOE_LAUNCH((sort_place_kernel<true>), dim3(G), dim3(1024), 0, st, s, G);
+  }
   return hipGetLastError();
 }
 
