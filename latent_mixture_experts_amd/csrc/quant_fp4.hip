@@ -58,8 +58,8 @@ __global__ __launch_bounds__(256) void fp4_quant_kernel(Fp4Quant p, int log_g, b
     const int row = row0 + u * rows_per_set;
     if (live_col && row < p.rows) {
       const size_t at = static_cast<size_t>(row) * p.ldx + col;
-      load8<F32>(p.x, at, v[u]);
-      if constexpr (SWIGLU) load8<F32>(p.x, at + p.cols, up[u]);
+      load8<F32, true>(p.x, at, v[u]);
+      if constexpr (SWIGLU) load8<F32, true>(p.x, at + p.cols, up[u]);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -166,7 +166,7 @@ __global__ __launch_bounds__(256) void fp4_dequant_kernel(Fp4Dequant p, int log_
       uint16_t* o = static_cast<uint16_t*>(p.out) + at;
       const uint4 q = __builtin_bit_cast(uint4, mxfp4x8_to_bf16(c[u], scale));
       if (wide) {
-        *reinterpret_cast<uint4*>(o) = q;
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, q), reinterpret_cast<u32x4*>(o));
       } else {
         const uint32_t d[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll

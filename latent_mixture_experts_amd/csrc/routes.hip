@@ -11,10 +11,13 @@
 // and its K routes' rows once each, which is the least there is; the rows of
 // one token lie anywhere, each in whole lines. Sums are fp32, over a token's
 // routes in rank order; nothing depends on the order in which workgroups run.
+#include <algorithm>
+
 #include "device_common.h"
 #include "kernels.h"
 #include "route_small.h"
 #include "routes.h"
+#include "silu.h"
 
 namespace moe {
 
@@ -214,152 +217,206 @@ __global__ __launch_bounds__(1024) void sort_place_kernel(SortRoutes s, int G) {
 }
 
 // ---- rows ------------------------------------------------------------------
-constexpr int kMaxK = 8;
+// A wavefront takes spans of kSpan columns of a token, eight values a lane: eight
+// neighbours where rows allow it (VEC), else 64 apart. Tokens start at different
+// spans: their rows lie a power of two apart as a rule, and wavefronts that walk
+// them in step meet on the same memory channels. Loads pass the caches by, which
+// leaves those to the rows on their way out (4096 tokens of 8 rows of 4096 bf16, in
+// one stream: sort, gather and its gradient 150 -> 121 us, combine and its gradient
+// 185 -> 162; stores that do so: 127 and 161, both: 125 and 168).
+constexpr int kMaxK = 8, kSpan = 512;
 
-template <bool F32, int V>
-__device__ __forceinline__ void load_row(const void* x, int64_t at, float v[V]) {
-  if constexpr (V == 1) {
-    v[0] = F32 ? static_cast<const float*>(x)[at] : bf16_to_f32(static_cast<const uint16_t*>(x)[at]);
-  } else if constexpr (F32) {
-#pragma unroll
-    for (int h = 0; h < V / 4; ++h) {
-      const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at + 4 * h);
-      v[4 * h] = a.x, v[4 * h + 1] = a.y, v[4 * h + 2] = a.z, v[4 * h + 3] = a.w;
-    }
+template <bool F32, bool VEC>
+__device__ __forceinline__ void load_span(const void* x, int64_t row, int c, int cols, float v[8]) {
+  if constexpr (VEC) {
+    load8<F32, true>(x, row + c, v);
   } else {
-    static_assert(V == 8, "16 bytes");
-    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
-    const uint32_t d[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(d[i] << 16);
-      v[2 * i + 1] = __uint_as_float(d[i] & 0xFFFF0000u);
+    for (int i = 0; i < 8; ++i) {
+      const int64_t at = row + c + 64 * i;
+      v[i] = 0.0f;
+      if (c + 64 * i < cols) v[i] = F32 ? static_cast<const float*>(x)[at] : bf16_to_f32(static_cast<const uint16_t*>(x)[at]);
     }
   }
 }
-template <bool F32, int V>
-__device__ __forceinline__ void store_row(void* x, int64_t at, const float v[V]) {
-  if constexpr (V == 1) {
-    if constexpr (F32)
-      static_cast<float*>(x)[at] = v[0];
-    else
-      static_cast<__bf16*>(x)[at] = static_cast<__bf16>(v[0]);
-  } else if constexpr (F32) {
+template <bool F32, bool VEC>
+__device__ __forceinline__ void store_span(void* x, int64_t row, int c, int cols, const float v[8]) {
+  if constexpr (VEC) {
+    if constexpr (F32) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(x) + row + c);
+      o[0] = float4{v[0], v[1], v[2], v[3]};
+      o[1] = float4{v[4], v[5], v[6], v[7]};
+    } else {
+      bf16x8 b;
 #pragma unroll
-    for (int h = 0; h < V / 4; ++h)
-      *reinterpret_cast<float4*>(static_cast<float*>(x) + at + 4 * h) = float4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+      for (int i = 0; i < 8; ++i) b[i] = static_cast<__bf16>(v[i]);
+      *reinterpret_cast<bf16x8*>(static_cast<uint16_t*>(x) + row + c) = b;
+    }
   } else {
-    bf16x8 b;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = static_cast<__bf16>(v[i]);
-    *reinterpret_cast<bf16x8*>(static_cast<uint16_t*>(x) + at) = b;
+    for (int i = 0; i < 8; ++i) {
+      const int64_t at = row + c + 64 * i;
+      if (c + 64 * i < cols) {
+        if constexpr (F32)
+          static_cast<float*>(x)[at] = v[i];
+        else
+          static_cast<__bf16*>(x)[at] = static_cast<__bf16>(v[i]);
+      }
+    }
   }
+}
+// A lane's first column in a span.
+template <bool VEC>
+__device__ __forceinline__ int span_column(int span, int lane) {
+  return span * kSpan + (VEC ? lane * 8 : lane);
 }
 
 // Rows from *n_taken on become zeros, by all workgroups.
-template <bool F32, int V>
+template <bool F32, bool VEC>
 __device__ __forceinline__ void zero_rest(const RouteRows& p) {
   if (!p.n_taken) return;
-  const float zero[V] = {};
+  const float zero[8] = {};
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, spans = (p.cols + kSpan - 1) / kSpan;
   for (int64_t r = static_cast<int64_t>(max(*p.n_taken, 0)) + blockIdx.x; r < p.rows; r += gridDim.x)
-    for (int c = threadIdx.x * V; c < p.cols; c += 256 * V) store_row<F32, V>(p.out, r * p.ldo + c, zero);
+    for (int s = wave; s < spans; s += 4) {
+      const int c = span_column<VEC>(s, lane);
+      if (c < p.cols) store_span<F32, VEC>(p.out, r * p.ldo, c, p.cols, zero);
+    }
 }
 
-// A token's rows; -1: none.
-__device__ __forceinline__ void positions_of(const RouteRows& p, int64_t t, int at[kMaxK]) {
+// A token's rows (-1: none) and, asked for, its weights: lane k loads those of
+// route k, and all of them go to scalar registers (one load's latency, not K).
+struct TokenRoutes {
+  int at[kMaxK];
+  float w[kMaxK];
+};
+template <bool WEIGHTS>
+__device__ __forceinline__ TokenRoutes routes_of(const RouteRows& p, int64_t t, int lane) {
+  const int v = lane < p.K ? p.positions[t * p.K + lane] : -1, mine = v >= 0 && v < p.rows ? v : -1;
+  const float w = WEIGHTS && p.w && lane < p.K ? p.w[t * p.K + lane] : 1.0f;
+  TokenRoutes r;
 #pragma unroll
   for (int k = 0; k < kMaxK; ++k) {
-    const int v = k < p.K ? p.positions[t * p.K + k] : -1;
-    at[k] = v >= 0 && v < p.rows ? v : -1;
+    r.at[k] = __builtin_amdgcn_readlane(mine, k);
+    r.w[k] = WEIGHTS ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), k)) : 1.0f;
+  }
+  return r;
+}
+
+// A workgroup's four wavefronts take 2^log spans of 4 >> log tokens, and
+// neighbouring workgroups the same tokens' next spans (nq workgroups to a set of
+// tokens), so that a row is read as a whole at about one time (combine, 4096 tokens
+// of 8 rows of 4096 bf16: by spans first 92 us).
+struct Walk {
+  int64_t token, step;  // first token of this wavefront, and to its next
+  int span;             // of `spans`, turned by the token; -1: none
+  int spans;
+};
+__device__ __forceinline__ Walk walk_of(const RouteRows& p, int wave, int log, int nq) {
+  Walk w;
+  w.spans = (p.cols + kSpan - 1) / kSpan;
+  const int set = static_cast<int>(blockIdx.x) / nq, q = static_cast<int>(blockIdx.x) - set * nq;
+  w.token = static_cast<int64_t>(set) * (4 >> log) + (wave >> log);
+  w.step = static_cast<int64_t>(gridDim.x / nq) * (4 >> log);
+  w.span = (q << log) + (wave & ((1 << log) - 1));
+  if (w.span >= w.spans) w.token = p.T;
+  return w;
+}
+
+template <bool F32, bool VEC>
+__global__ __launch_bounds__(256) void gather_rows_kernel(RouteRows p, int log, int nq) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Walk walk = walk_of(p, wave, log, nq);
+  for (int64_t t = walk.token; t < p.T; t += walk.step) {
+    const TokenRoutes r = routes_of<false>(p, t, lane);
+    const int c = span_column<VEC>(static_cast<int>((walk.span + t) % walk.spans), lane);
+    if (c >= p.cols) continue;
+    float v[8];
+    load_span<F32, VEC>(p.x, t * p.ldx, c, p.cols, v);
+#pragma unroll
+    for (int k = 0; k < kMaxK; ++k)
+      if (r.at[k] >= 0) store_span<F32, VEC>(p.out, r.at[k] * p.ldo, c, p.cols, v);
+  }
+  zero_rest<F32, VEC>(p);
+}
+
+template <bool XF32, bool OF32, bool VEC>
+__global__ __launch_bounds__(256) void combine_rows_kernel(RouteRows p, int log, int nq) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Walk walk = walk_of(p, wave, log, nq);
+  for (int64_t t = walk.token; t < p.T; t += walk.step) {
+    const TokenRoutes r = routes_of<true>(p, t, lane);
+    const int c = span_column<VEC>(static_cast<int>((walk.span + t) % walk.spans), lane);
+    if (c >= p.cols) continue;
+    float v[kMaxK][8], sum[8] = {};
+#pragma unroll
+    for (int k = 0; k < kMaxK; ++k)
+      if (r.at[k] >= 0) load_span<XF32, VEC>(p.x, r.at[k] * p.ldx, c, p.cols, v[k]);
+#pragma unroll
+    for (int k = 0; k < kMaxK; ++k)
+      if (r.at[k] >= 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = fmaf(r.w[k], v[k][i], sum[i]);
+      }
+    store_span<OF32, VEC>(p.out, t * p.ldo, c, p.cols, sum);
   }
 }
 
-// One wavefront per token, over the columns.
-template <bool F32, int V>
-__global__ __launch_bounds__(256) void gather_rows_kernel(RouteRows p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave; t < p.T; t += static_cast<int64_t>(gridDim.x) * 4) {
-    int at[kMaxK];
-    positions_of(p, t, at);
-    for (int c = lane * V; c < p.cols; c += 64 * V) {
-      float v[V];
-      load_row<F32, V>(p.x, t * p.ldx + c, v);
-#pragma unroll
-      for (int k = 0; k < kMaxK; ++k)
-        if (at[k] >= 0) store_row<F32, V>(p.out, at[k] * p.ldo + c, v);
-    }
-  }
-  zero_rest<F32, V>(p);
-}
-
-template <bool XF32, bool OF32, int V>
-__global__ __launch_bounds__(256) void combine_rows_kernel(RouteRows p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave; t < p.T; t += static_cast<int64_t>(gridDim.x) * 4) {
-    int at[kMaxK];
-    positions_of(p, t, at);
-    float w[kMaxK];
-#pragma unroll
-    for (int k = 0; k < kMaxK; ++k) w[k] = at[k] >= 0 && p.w ? p.w[t * p.K + k] : 1.0f;
-    for (int c = lane * V; c < p.cols; c += 64 * V) {
-      float v[kMaxK][V], sum[V] = {};
-#pragma unroll
-      for (int k = 0; k < kMaxK; ++k)
-        if (at[k] >= 0) load_row<XF32, V>(p.x, at[k] * p.ldx + c, v[k]);
-#pragma unroll
-      for (int k = 0; k < kMaxK; ++k)
-        if (at[k] >= 0) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) sum[i] = fmaf(w[k], v[k][i], sum[i]);
-        }
-      store_row<OF32, V>(p.out, t * p.ldo + c, sum);
-    }
-  }
-}
-
-template <bool XF32, bool GF32, int V>
+// WPT wavefronts to a token: 4, or 1 where a token has one span. A token's dot
+// products are joined over the lanes, then over the wavefronts in order.
+template <bool XF32, bool GF32, bool VEC, int WPT>
 __global__ __launch_bounds__(256) void combine_backward_kernel(RouteRows p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + wave; t < p.T; t += static_cast<int64_t>(gridDim.x) * 4) {
-    int at[kMaxK];
-    positions_of(p, t, at);
-    float w[kMaxK], dot[kMaxK] = {};
-#pragma unroll
-    for (int k = 0; k < kMaxK; ++k) w[k] = at[k] >= 0 && p.w ? p.w[t * p.K + k] : 1.0f;
-    for (int c = lane * V; c < p.cols; c += 64 * V) {
-      float g[V], v[kMaxK][V];
-      load_row<GF32, V>(p.grad, t * p.ldg + c, g);
+  __shared__ float part[WPT][kMaxK];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr int kTokens = 4 / WPT;
+  const int spans = (p.cols + kSpan - 1) / kSpan;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + wave / WPT; t < p.T; t += static_cast<int64_t>(gridDim.x) * kTokens) {
+    const TokenRoutes r = routes_of<true>(p, t, lane);
+    float dot[kMaxK] = {};
+    for (int s = wave % WPT; s < spans; s += WPT) {
+      const int c = span_column<VEC>(static_cast<int>((s + t) % spans), lane);
+      if (c >= p.cols) continue;
+      float g[8], v[kMaxK][8];
+      load_span<GF32, VEC>(p.grad, t * p.ldg, c, p.cols, g);
       if (p.dw) {
 #pragma unroll
         for (int k = 0; k < kMaxK; ++k)
-          if (at[k] >= 0) load_row<XF32, V>(p.x, at[k] * p.ldx + c, v[k]);
+          if (r.at[k] >= 0) load_span<XF32, VEC>(p.x, r.at[k] * p.ldx, c, p.cols, v[k]);
 #pragma unroll
         for (int k = 0; k < kMaxK; ++k)
-          if (at[k] >= 0) {
+          if (r.at[k] >= 0) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) dot[k] = fmaf(v[k][i], g[i], dot[k]);
+            for (int i = 0; i < 8; ++i) dot[k] = fmaf(v[k][i], g[i], dot[k]);
           }
       }
       if (p.out) {
 #pragma unroll
         for (int k = 0; k < kMaxK; ++k)
-          if (at[k] >= 0) {
-            float d[V];
+          if (r.at[k] >= 0) {
+            float d[8];
 #pragma unroll
-            for (int i = 0; i < V; ++i) d[i] = w[k] * g[i];
-            store_row<XF32, V>(p.out, at[k] * p.ldo + c, d);
+            for (int i = 0; i < 8; ++i) d[i] = r.w[k] * g[i];
+            store_span<XF32, VEC>(p.out, r.at[k] * p.ldo, c, p.cols, d);
           }
       }
     }
     if (p.dw) {
+      float sum = 0.0f;  // lane k: route k's
 #pragma unroll
       for (int k = 0; k < kMaxK; ++k) {
-        const float sum = wave_sum_f32(dot[k]);
-        if (k < p.K && lane == 0) p.dw[t * p.K + k] = sum;
+        const float all = wave_sum_f32(dot[k]);
+        sum = lane == k ? all : sum;
       }
+      if constexpr (WPT > 1) {
+        if (lane < kMaxK) part[wave][lane] = sum;
+        __syncthreads();
+        if (wave == 0 && lane < kMaxK) sum = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+        __syncthreads();  // (the next token's are written then)
+      }
+      if (wave % WPT == 0 && lane < p.K) p.dw[t * p.K + lane] = sum;
     }
   }
-  if (p.out) zero_rest<XF32, V>(p);
+  if (p.out) zero_rest<XF32, VEC>(p);
 }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -371,7 +428,20 @@ bool eights(const RouteRows& p) {
          aligned16(p.grad);
 }
 
-dim3 token_grid(int T) { return dim3(static_cast<unsigned>(T < 1 ? 1 : T < (1 << 22) ? (T + 3) / 4 : 1 << 20)); }
+constexpr int kMostBlocks = 1 << 22;  // (a launch holds fewer than 2^32 threads)
+
+// Workgroups of `tokens` tokens each, nq to one set of them; more tokens than that
+// take turns.
+int token_grid(int T, int tokens, int nq) { return nq * std::max(1, std::min((T + tokens - 1) / tokens, kMostBlocks / nq)); }
+
+struct Spans {
+  int log, nq;
+  explicit Spans(int cols) {
+    const int spans = (cols + kSpan - 1) / kSpan;
+    log = spans >= 3 ? 2 : spans - 1;
+    nq = (spans + (1 << log) - 1) >> log;
+  }
+};
 
 }  // namespace
 
@@ -397,31 +467,37 @@ hipError_t launch_sort_routes(const SortRoutes& s, hipStream_t st) {
 }
 
 hipError_t launch_gather_rows(const RouteRows& p, hipStream_t st) {
-  const dim3 grid = token_grid(p.T), block(256);
+  const Spans sp(p.cols);
+  const dim3 grid(token_grid(p.T, 4 >> sp.log, sp.nq)), block(256);
   if (p.x_f32)
-    eights(p) ? MOE_LAUNCH((gather_rows_kernel<true, 8>), grid, block, 0, st, p)
-              : MOE_LAUNCH((gather_rows_kernel<true, 1>), grid, block, 0, st, p);
+    eights(p) ? MOE_LAUNCH((gather_rows_kernel<true, true>), grid, block, 0, st, p, sp.log, sp.nq)
+              : MOE_LAUNCH((gather_rows_kernel<true, false>), grid, block, 0, st, p, sp.log, sp.nq);
   else
-    eights(p) ? MOE_LAUNCH((gather_rows_kernel<false, 8>), grid, block, 0, st, p)
-              : MOE_LAUNCH((gather_rows_kernel<false, 1>), grid, block, 0, st, p);
+    eights(p) ? MOE_LAUNCH((gather_rows_kernel<false, true>), grid, block, 0, st, p, sp.log, sp.nq)
+              : MOE_LAUNCH((gather_rows_kernel<false, false>), grid, block, 0, st, p, sp.log, sp.nq);
   return hipGetLastError();
 }
 
-template <bool XF32, bool OF32>
+template <bool XF32, bool OF32, bool VEC>
 static void combine_as(const RouteRows& p, bool backward, hipStream_t st) {
-  const dim3 grid = token_grid(p.T), block(256);
-  if (backward)
-    eights(p) ? MOE_LAUNCH((combine_backward_kernel<XF32, OF32, 8>), grid, block, 0, st, p)
-              : MOE_LAUNCH((combine_backward_kernel<XF32, OF32, 1>), grid, block, 0, st, p);
+  const Spans sp(p.cols);
+  const dim3 block(256);
+  if (!backward)
+    MOE_LAUNCH((combine_rows_kernel<XF32, OF32, VEC>), dim3(token_grid(p.T, 4 >> sp.log, sp.nq)), block, 0, st, p, sp.log, sp.nq);
+  else if (p.cols > kSpan)
+    MOE_LAUNCH((combine_backward_kernel<XF32, OF32, VEC, 4>), dim3(token_grid(p.T, 1, 1)), block, 0, st, p);
   else
-    eights(p) ? MOE_LAUNCH((combine_rows_kernel<XF32, OF32, 8>), grid, block, 0, st, p)
-              : MOE_LAUNCH((combine_rows_kernel<XF32, OF32, 1>), grid, block, 0, st, p);
+    MOE_LAUNCH((combine_backward_kernel<XF32, OF32, VEC, 1>), dim3(token_grid(p.T, 4, 1)), block, 0, st, p);
+}
+template <bool XF32, bool OF32>
+static void combine_types(const RouteRows& p, bool backward, hipStream_t st) {
+  eights(p) ? combine_as<XF32, OF32, true>(p, backward, st) : combine_as<XF32, OF32, false>(p, backward, st);
 }
 static hipError_t combine(const RouteRows& p, bool backward, hipStream_t st) {
   if (p.x_f32)
-    p.out_f32 ? combine_as<true, true>(p, backward, st) : combine_as<true, false>(p, backward, st);
+    p.out_f32 ? combine_types<true, true>(p, backward, st) : combine_types<true, false>(p, backward, st);
   else
-    p.out_f32 ? combine_as<false, true>(p, backward, st) : combine_as<false, false>(p, backward, st);
+    p.out_f32 ? combine_types<false, true>(p, backward, st) : combine_types<false, false>(p, backward, st);
   return hipGetLastError();
 }
 hipError_t launch_combine_rows(const RouteRows& p, hipStream_t st) { return combine(p, false, st); }

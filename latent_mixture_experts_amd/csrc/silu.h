@@ -37,15 +37,23 @@ __device__ __forceinline__ float silu_times(float g, float u) {
   }
 }
 
-// Eight consecutive values.
-template <bool F32>
+// Eight consecutive values. STREAM: values that nothing reads again soon pass the
+// caches by (non-temporal).
+template <bool STREAM>
+__device__ __forceinline__ uint4 load16(const void* p) {
+  if constexpr (STREAM)
+    return __builtin_bit_cast(uint4, __builtin_nontemporal_load(static_cast<const u32x4*>(p)));
+  else
+    return *static_cast<const uint4*>(p);
+}
+template <bool F32, bool STREAM = false>
 __device__ __forceinline__ void load8(const void* x, size_t at, float v[8]) {
   if constexpr (F32) {
-    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-    const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at + 4);
+    const float4 a = __builtin_bit_cast(float4, load16<STREAM>(static_cast<const float*>(x) + at));
+    const float4 b = __builtin_bit_cast(float4, load16<STREAM>(static_cast<const float*>(x) + at + 4));
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
+    const uint4 a = load16<STREAM>(static_cast<const uint16_t*>(x) + at);
     const uint32_t d[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
