@@ -8,6 +8,7 @@
 namespace moe {
 
 constexpr int kFp4Group = 32;  // values per scale
+enum { kBy16, kBy4, kBy1 };    // how many scales of a row one copy may take
 
 // rows x cols values (bf16, or fp32 when f32) to codes [rows][cols/2] and
 // scales [rows][cols/32]; swiglu: x rows hold 2 * cols values, cols gate then
@@ -51,7 +52,7 @@ struct Fp4Gemm {
   bool f32;       // out fp32, else bf16
   bool out_vec;   // out rows take four-value stores (base and pitch aligned)
   bool out_vec8;  // and eight-value ones (bf16)
-  bool scale_vec; // scale rows start at multiples of 16 bytes, in x and w
+  int scales;     // kBy16, kBy4: scale rows start at multiples of 16, 4 bytes, in x and w
 };
 hipError_t launch_fp4_gemm(const Fp4Gemm& g, hipStream_t st);
 

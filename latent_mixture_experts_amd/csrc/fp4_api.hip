@@ -80,7 +80,8 @@ Fp4Gemm product(int32_t rows, int32_t N, int32_t K, const uint8_t* x, int64_t ld
   g.f32 = type == MOE_TYPE_F32;
   g.out_vec = ldo % 4 == 0 && aligned(out, g.f32 ? 16 : 8);
   g.out_vec8 = !g.f32 && ldo % 8 == 0 && aligned(out, 16);
-  g.scale_vec = K % (16 * kFp4Group) == 0 && aligned(xs, 16) && aligned(ws, 16);
+  const auto start_at = [&](int n) { return K / kFp4Group % n == 0 && aligned(xs, n) && aligned(ws, n); };
+  g.scales = start_at(16) ? kBy16 : start_at(4) ? kBy4 : kBy1;
   return g;
 }
 

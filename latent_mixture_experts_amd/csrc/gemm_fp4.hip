@@ -142,10 +142,10 @@ __global__ __launch_bounds__(64 * kFW, 2) void fp4_stream_kernel(Fp4Gemm p) {
 // row r lies at place (g + 4i) ^ ((r/2) % 8) of the row's eight, so that the rows
 // one read touches start in distinct banks (in the order of the pieces half the
 // banks met twice: 4096 x 4096 x 8192 81 -> 79 us).
-// Scales: where the rows' scales start at multiples of 16 bytes (WIDE), 16 bytes
-// per copy, the scales of 512 values of a row: of two stages (KG = 1, two such
-// sets in turn), or of (half of) one. Else byte by byte, each into a word of its
-// own, with the codes they belong to.
+// Scales: in sets of 16 bytes, the scales of 512 values of a row: of two stages (KG
+// = 1, two such sets in turn), or of (half of) one; 16 bytes per copy where rows'
+// scales start at multiples of 16 bytes (kBy16), else of 4 (kBy4). Else (kBy1) byte
+// by byte, each into a word of its own, with the codes they belong to.
 constexpr int kBlockValues = 256, kRowBytes = 128, kPieces = 8;  // of a row and block
 
 __device__ __forceinline__ int piece_at(int r, int c) { return (r * 8 + ((c >> 1 | (c & 1) << 2) ^ ((r >> 1) & 7))) * 16; }
@@ -174,9 +174,10 @@ __device__ __forceinline__ void lds_copy1(rsrc_t r, uint32_t voff, uint32_t lds)
   asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_ubyte %0, %1, 0 offen lds" ::"v"(voff), "s"(r), "s"(lds) : "memory");
 }
 
-template <int WT, int WW, int FT, int FW, int R, int KG, bool WIDE, bool EARLY, bool ONCE>
+template <int WT, int WW, int FT, int FW, int R, int KG, int SCALES, bool EARLY, bool ONCE>
 __global__ __launch_bounds__(64 * WT * WW * KG) void fp4_tile_kernel(Fp4Gemm p, int n_row_tiles, int n_col_tiles, int chunk) {
   constexpr int kGroup = WT * WW, NW = kGroup * KG, BM = WT * FT * 16, BN = WW * FW * 16;
+  constexpr bool WIDE = SCALES != kBy1;
   // 1-KiB copies per wavefront and stage (its group's block); of the rows' some
   // wavefronts may have one fewer
   constexpr int kXOps = (BM / 8 + kGroup - 1) / kGroup, kXLeast = BM / 8 / kGroup, kWOps = BN / 8 / kGroup;
@@ -185,13 +186,13 @@ __global__ __launch_bounds__(64 * WT * WW * KG) void fp4_tile_kernel(Fp4Gemm p, 
   static_assert(kWOps * 8 * kGroup == BN && kXLeast > 0, "whole copies");
   static_assert(R >= 2 && R <= 4 && (R - 2) * kLeast < 64, "vmcnt field; scale sets land in time");
   constexpr int kXSlot = KG * BM * kRowBytes, kWSlot = KG * BN * kRowBytes;  // bytes of a stage
-  // scale sets: stages of one, sets held, 16-byte halves of a row, copies of 64 rows
+  // scale sets: stages of one, sets held, 16-byte halves of a row, blocks of 64 rows, copies of one
   constexpr bool kPairs = WIDE && KG == 1;
-  constexpr int kSets = kPairs ? 2 : R, kHalves = WIDE && KG == 4 ? 2 : 1;
+  constexpr int kSets = kPairs ? 2 : R, kHalves = WIDE && KG == 4 ? 2 : 1, kParts = SCALES == kBy4 ? 4 : 1;
   constexpr int kXC = (BM + 63) / 64, kWC = (BN + 63) / 64;
   constexpr int kSxSlot = WIDE ? kHalves * kXC * 1024 : KG * BM * kPieces * 4;
   constexpr int kSwSlot = WIDE ? kHalves * kWC * 1024 : KG * BN * kPieces * 4;
-  constexpr int kSOps = (kHalves * (kXC + kWC) + NW - 1) / NW;  // WIDE: copies per wavefront and set
+  constexpr int kSOps = (kParts * kHalves * (kXC + kWC) + NW - 1) / NW;  // WIDE: copies per wavefront and set
   __shared__ __attribute__((aligned(1024))) uint8_t Xs[R][kXSlot];
   __shared__ __attribute__((aligned(1024))) uint8_t Ws[R][kWSlot];
   __shared__ __attribute__((aligned(1024))) uint8_t Sx[kSets][kSxSlot];
@@ -228,6 +229,12 @@ __global__ __launch_bounds__(64 * WT * WW * KG) void fp4_tile_kernel(Fp4Gemm p, 
   const rsrc_t xs_r = make_rsrc(p.xs + static_cast<size_t>(base) * kscales, static_cast<uint32_t>(xrows) * kscales);
   auto row_of = [&](int r) -> int { return r < nrows ? source_row(p, grp.begin + r) - base : -1; };
 
+  // Copy o of a scale set: of half `half` of block `block` of 64 rows (the rows', then
+  // the weights'), all of them, or 16 with a word per lane.
+  struct SetCopy {
+    int block, half, part;
+    __device__ __forceinline__ explicit SetCopy(int o) : block(o / kParts / kHalves), half(o / kParts % kHalves), part(o % kParts) {}
+  };
   // Source offsets of this wavefront's copies in the first stage; the
   // descriptors of the codes step along K, so a copy costs no vector arithmetic.
   uint32_t xoff[kXOps], woff[kWOps];
@@ -247,10 +254,10 @@ __global__ __launch_bounds__(64 * WT * WW * KG) void fp4_tile_kernel(Fp4Gemm p, 
   if constexpr (WIDE) {
 #pragma unroll
     for (int i = 0; i < kSOps; ++i) {
-      const int o = i * NW + wave, c = o / kHalves, half = o % kHalves;  // (rows' copies, then weights')
-      const int r = (c < kXC ? c : c - kXC) * 64 + lane;
-      const int src = c < kXC ? row_of(r) : r < ncols ? r : -1;
-      soff[i] = src < 0 ? kOutOfRange : static_cast<uint32_t>(src * kscales + half * 16);
+      const SetCopy o(i * NW + wave);
+      const int r = (o.block < kXC ? o.block : o.block - kXC) * 64 + (SCALES == kBy4 ? o.part * 16 + lane / 4 : lane);
+      const int src = o.block < kXC ? row_of(r) : r < ncols ? r : -1;
+      soff[i] = src < 0 ? kOutOfRange : static_cast<uint32_t>(src * kscales + o.half * 16 + (SCALES == kBy4 ? lane % 4 * 4 : 0));
     }
   }
   const uint32_t lds_x = lds_address(&Xs[0][0]), lds_w = lds_address(&Ws[0][0]);
@@ -320,13 +327,19 @@ __global__ __launch_bounds__(64 * WT * WW * KG) void fp4_tile_kernel(Fp4Gemm p, 
     if constexpr (WIDE) {
 #pragma unroll
       for (int i = 0; i < kSOps; ++i) {
-        const int o = i * NW + wave, c = o / kHalves, half = o % kHalves;
-        const int s0 = (set * kHalves + half) * 16;  // first scale
+        const SetCopy o(i * NW + wave);
+        const int s0 = (set * kHalves + o.half) * 16 + (SCALES == kBy4 ? lane % 4 * 4 : 0);  // first scale
         const uint32_t off = s0 < kscales ? soff[i] + set * (kHalves * 16) : kOutOfRange;
-        if (c < kXC)
-          lds_copy16(xs_r, off, __builtin_amdgcn_readfirstlane(lds_sx + at * kSxSlot + half * (kXC * 1024) + c * 1024));
-        else if (c < kXC + kWC)
-          lds_copy16(ws_r, off, __builtin_amdgcn_readfirstlane(lds_sw + at * kSwSlot + half * (kWC * 1024) + (c - kXC) * 1024));
+        const bool of_x = o.block < kXC;
+        if (of_x || o.block < kXC + kWC) {
+          const uint32_t to = __builtin_amdgcn_readfirstlane(
+              (of_x ? lds_sx + at * kSxSlot + o.half * (kXC * 1024) + o.block * 1024
+                    : lds_sw + at * kSwSlot + o.half * (kWC * 1024) + (o.block - kXC) * 1024) + o.part * 256);
+          if constexpr (SCALES == kBy4)
+            of_x ? lds_copy4(xs_r, off, to) : lds_copy4(ws_r, off, to);
+          else
+            of_x ? lds_copy16(xs_r, off, to) : lds_copy16(ws_r, off, to);
+        }
       }
     }
   };
@@ -563,7 +576,7 @@ __global__ __launch_bounds__(64 * WT * WW * KG) void fp4_tile_kernel(Fp4Gemm p, 
 
 template <int KS, int D, bool F32>
 void launch_stream_as(const Fp4Gemm& g, dim3 grid, hipStream_t st) {
-  if (g.scale_vec)
+  if (g.scales == kBy16)
     MOE_LAUNCH((fp4_stream_kernel<KS, D, F32, true>), grid, dim3(64 * kFW), 0, st, g);
   else
     MOE_LAUNCH((fp4_stream_kernel<KS, D, F32, false>), grid, dim3(64 * kFW), 0, st, g);
@@ -586,7 +599,7 @@ hipError_t launch_stream(const Fp4Gemm& g, hipStream_t st) {
   return launch_stream_ks<8, 2>(g, tiles, st);
 }
 
-template <int WT, int WW, int FT, int FW, int R, int KG, bool WIDE, bool EARLY = false>
+template <int WT, int WW, int FT, int FW, int R, int KG, int SCALES, bool EARLY = false>
 hipError_t launch_tile_as(const Fp4Gemm& g, hipStream_t st) {
   constexpr int BM = WT * FT * 16, BN = WW * FW * 16;
   const int nct = (g.N + BN - 1) / BN;
@@ -601,17 +614,20 @@ hipError_t launch_tile_as(const Fp4Gemm& g, hipStream_t st) {
     grid = (nrt * nct + 7) / 8 * 8;
   }
   // Weights that about one row tile reads pass the caches by (32 tokens' down
-  // projection 246 -> 225 us, 4096 tokens' 575 -> 550); 4096 dense rows would lose 5%.
+  // projection 246 -> 225 us, 4096 tokens' 575 -> 535); 4096 dense rows would lose 5%.
   const dim3 block(64 * WT * WW * KG);
-  if (g.rows <= static_cast<int64_t>(BM) * g.experts)
-    MOE_LAUNCH((fp4_tile_kernel<WT, WW, FT, FW, R, KG, WIDE, EARLY, true>), dim3(grid), block, 0, st, g, nrt, nct, chunk);
+  if (SCALES != kBy1 && g.rows <= static_cast<int64_t>(BM) * g.experts)
+    MOE_LAUNCH((fp4_tile_kernel<WT, WW, FT, FW, R, KG, SCALES, EARLY, SCALES != kBy1>), dim3(grid), block, 0, st, g, nrt, nct, chunk);
   else
-    MOE_LAUNCH((fp4_tile_kernel<WT, WW, FT, FW, R, KG, WIDE, EARLY, false>), dim3(grid), block, 0, st, g, nrt, nct, chunk);
+    MOE_LAUNCH((fp4_tile_kernel<WT, WW, FT, FW, R, KG, SCALES, EARLY, false>), dim3(grid), block, 0, st, g, nrt, nct, chunk);
   return hipGetLastError();
 }
-template <int WT, int WW, int FT, int FW, int R, int KG>
+// RB: stages held with scales by bytes, which take more LDS.
+template <int WT, int WW, int FT, int FW, int R, int KG, int RB = R, bool EARLY = false>
 hipError_t launch_tile(const Fp4Gemm& g, hipStream_t st) {
-  return g.scale_vec ? launch_tile_as<WT, WW, FT, FW, R, KG, true>(g, st) : launch_tile_as<WT, WW, FT, FW, R, KG, false>(g, st);
+  if (g.scales == kBy16) return launch_tile_as<WT, WW, FT, FW, R, KG, kBy16, EARLY>(g, st);
+  if (g.scales == kBy4) return launch_tile_as<WT, WW, FT, FW, R, KG, kBy4, EARLY>(g, st);
+  return launch_tile_as<WT, WW, FT, FW, RB, KG, kBy1>(g, st);
 }
 
 // The tiles: rows, weight rows, and what one takes in ns: start and end, and per
@@ -641,7 +657,6 @@ struct TileShape {
   TileCost wide, bytes;
 };
 enum { T32x32, T32x64, T64x64, T64x128, T128x128, T128x128Two, T128x256, T256x256, kNTiles };
-constexpr double kNever = 1e9;  // (256 x 256 by bytes: too few registers)
 constexpr TileShape kTiles[kNTiles] = {{32, 32, {1, 4800, 160, 160}, {1, 4800, 180, 180}},
                                        {32, 64, {2, 3500, 320, 510}, {1, 3500, 430, 430}},
                                        {64, 64, {1, 4800, 340, 340}, {1, 4800, 550, 550}},
@@ -649,7 +664,7 @@ constexpr TileShape kTiles[kNTiles] = {{32, 32, {1, 4800, 160, 160}, {1, 4800, 1
                                        {128, 128, {1, 5700, 680, 680}, {1, 5700, 1090, 1090}},
                                        {128, 128, {2, 5000, 850, 1300}, {2, 3800, 1540, 2100}},
                                        {128, 256, {1, 6600, 1140, 1140}, {1, 6600, 2270, 2270}},
-                                       {256, 256, {1, 8100, 1850, 1850}, {1, 0, kNever, kNever}}};
+                                       {256, 256, {1, 8100, 1850, 1850}, {1, 8100, 1850, 1850}}};
 
 int best_tile(const Fp4Gemm& g) {
   // rows of one group: experts get theirs unevenly, by about the root of the mean
@@ -663,7 +678,8 @@ int best_tile(const Fp4Gemm& g) {
     const TileShape& t = kTiles[i];
     const double per_group = std::ceil(std::max(rows, 1.0) / t.rows);
     const double tiles = groups * per_group * std::ceil(static_cast<double>(g.N) / t.cols);
-    const TileCost& c = g.scale_vec ? t.wide : t.bytes;
+    if (i == T256x256 && g.scales != kBy16) continue;  // (no registers to spare)
+    const TileCost& c = g.scales == kBy1 ? t.bytes : t.wide;
     const double round = 256.0 * c.per_cu, whole = std::floor(tiles / round), rest = tiles - whole * round;
     const double full = c.ends + blocks * c.full, one = c.ends + blocks * c.one;
     const double ns = whole * full + (rest == 0 ? 0 : rest <= 256 ? one : full);
@@ -702,11 +718,9 @@ hipError_t launch_fp4_gemm(const Fp4Gemm& g, hipStream_t st) {
     case T64x64: return launch_tile<2, 2, 2, 2, 3, 2>(g, st);
     case T64x128: return launch_tile<2, 4, 2, 2, 3, 1>(g, st);
     case T128x128: return launch_tile<2, 4, 4, 2, 3, 1>(g, st);
-    case T128x128Two:
-      return g.scale_vec ? launch_tile_as<2, 2, 4, 4, 2, 1, true, true>(g, st) : launch_tile_as<2, 2, 4, 4, 2, 1, false>(g, st);
-    case T256x256: return launch_tile_as<4, 2, 4, 8, 2, 1, true, true>(g, st);
-    default:
-      return g.scale_vec ? launch_tile_as<2, 4, 4, 4, 3, 1, true>(g, st) : launch_tile_as<2, 4, 4, 4, 2, 1, false>(g, st);
+    case T128x128Two: return launch_tile<2, 2, 4, 4, 2, 1, 2, true>(g, st);
+    case T128x256: return launch_tile<2, 4, 4, 4, 3, 1, 2>(g, st);
+    default: return launch_tile_as<4, 2, 4, 8, 2, 1, kBy16, true>(g, st);  // (by 16 only: no registers to spare)
   }
 }
 

@@ -190,6 +190,15 @@ def test_linear(T, N, K, dtype):
     check(B.fp4_linear(*(t.cuda() for t in ops), dtype), *ops, dtype)
 
 
+@pytest.mark.parametrize("K", [128, 416, 640, 896, 1024, 1408, 2560])
+@pytest.mark.parametrize("T,N", [(9, 4096), (64, 4096), (128, 4096), (250, 4096), (500, 4000), (1024, 4096), (2000, 4096),
+                                 (1000, 8190), (4096, 4096)])
+def test_linear_every_tile_and_copy_of_scales(T, N, K):
+    """Row counts at which each tile is taken, widths whose scale rows start at multiples of 16, of 4 and of 1 bytes."""
+    ops = operands(T, N, K, gen(T + N + K))
+    check(B.fp4_linear(*(t.cuda() for t in ops)), *ops, torch.bfloat16)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T", [1, 5, 16, 40, 300])
 def test_linear_wide_scales(T, dtype):
