@@ -9,6 +9,12 @@
 // added in fp32 (measured: 128 products with scales of 2^-27 .. 2^23 are within
 // 6.5e-8 of their sizes, denormal and vanishing results as IEEE rounding gives
 // them, a scale of 255 gives NaN).
+//
+// What bounds it: one to 16 rows, the weights' way from HBM and a launch's start
+// (4096 x 8192: 6.4 us); few rows per expert, HBM (32 tokens' down projection, 163
+// experts of 4096 x 4096, 1.45 GB: 219 us, 6.6 TB/s); thousands of rows, the
+// operands' way from L2 into LDS (4096 x 4096 x 8192: 67 us, 4.1 PFLOP/s, of which
+// the matrix unit is busy 27 us at 2.4 GHz; 806 MB pass into LDS at 12 TB/s).
 #include <algorithm>
 #include <cmath>
 
@@ -613,8 +619,9 @@ hipError_t launch_tile_as(const Fp4Gemm& g, hipStream_t st) {
   } else {
     grid = (nrt * nct + 7) / 8 * 8;
   }
-  // Weights that about one row tile reads pass the caches by (32 tokens' down
-  // projection 246 -> 225 us, 4096 tokens' 575 -> 535); 4096 dense rows would lose 5%.
+  // Weights that about one row tile reads pass the caches by (down projection with
+  // its quantisation, 32 tokens 246 -> 225 us, 4096 tokens 677 -> 643); weights that
+  // many tiles read do not (4096 dense rows 93 -> 99).
   const dim3 block(64 * WT * WW * KG);
   if (SCALES != kBy1 && g.rows <= static_cast<int64_t>(BM) * g.experts)
     MOE_LAUNCH((fp4_tile_kernel<WT, WW, FT, FW, R, KG, SCALES, EARLY, SCALES != kBy1>), dim3(grid), block, 0, st, g, nrt, nct, chunk);

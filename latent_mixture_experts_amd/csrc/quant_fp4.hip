@@ -14,7 +14,10 @@
 // Memory bound: each value is read once and held in registers between maximum
 // and conversion. A lane holds 8 values (16-byte loads of bf16, 4-byte stores),
 // a group is four lanes, its maximum two DPP steps, the conversion instruction
-// takes the scale.
+// takes the scale. Loads of values, and stores of them on the way back, pass the
+// caches by (4096 x 8192 there and back 31.4 -> 30.4 us, SwiGLU 2% less). 4096 x 8192
+// bf16: 16 us, 5.3 TB/s, and back 12 us (codes from the cache); SwiGLU to 32768 x
+// 4096 bf16 101 us, 6.0 TB/s; 32 x 4096: 2.2 us, a launch.
 #include "device_common.h"
 #include "fp4.h"
 #include "kernels.h"

@@ -37,7 +37,7 @@ namespace {
 // turns the counts into places first (longer runs: fewer counts to write and
 // read). All latency: 64 routes 4.0 us, 3000 8, 32768 8.5 (runs of two steps 11.3),
 // 262136 13.3; 8 million 125 us (runs of one step 167).
-constexpr int kSortWaves = 16, kOneGroup = 3072, kFewRoutes = 1 << 18, kExperts = 256;
+constexpr int kSortWaves = 16, kOneGroup = 2560, kFewRoutes = 1 << 18, kExperts = 256;
 constexpr int kShortRun = 64, kLongRun = 256;
 __host__ __device__ constexpr int chunk_of(int R) { return kSortWaves * (R <= kFewRoutes ? kShortRun : kLongRun); }
 
