@@ -12,6 +12,7 @@
 // one token lie anywhere, each in whole lines. Sums are fp32, over a token's
 // routes in rank order; nothing depends on the order in which workgroups run.
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
 #include "kernels.h"
@@ -329,19 +330,41 @@ __device__ __forceinline__ Walk walk_of(const RouteRows& p, int wave, int log, i
   return w;
 }
 
+// (bits as they are: no conversion on the way)
 template <bool F32, bool VEC>
 __global__ __launch_bounds__(256) void gather_rows_kernel(RouteRows p, int log, int nq) {
+  using Bits = std::conditional_t<F32, uint32_t, uint16_t>;
+  constexpr int kWords = F32 ? 2 : 1;  // 16-byte pieces of eight values
+  const Bits* x = static_cast<const Bits*>(p.x);
+  Bits* out = static_cast<Bits*>(p.out);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Walk walk = walk_of(p, wave, log, nq);
   for (int64_t t = walk.token; t < p.T; t += walk.step) {
     const TokenRoutes r = routes_of<false>(p, t, lane);
     const int c = span_column<VEC>(static_cast<int>((walk.span + t) % walk.spans), lane);
     if (c >= p.cols) continue;
-    float v[8];
-    load_span<F32, VEC>(p.x, t * p.ldx, c, p.cols, v);
+    uint4 piece[kWords];
+    Bits v[8];
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) piece[i] = load16<true>(x + t * p.ldx + c + i * (16 / sizeof(Bits)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = c + 64 * i < p.cols ? x[t * p.ldx + c + 64 * i] : 0;
+    }
 #pragma unroll
     for (int k = 0; k < kMaxK; ++k)
-      if (r.at[k] >= 0) store_span<F32, VEC>(p.out, r.at[k] * p.ldo, c, p.cols, v);
+      if (r.at[k] >= 0) {
+        Bits* o = out + r.at[k] * p.ldo + c;
+        if constexpr (VEC) {
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) *reinterpret_cast<uint4*>(o + i * (16 / sizeof(Bits))) = piece[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + 64 * i < p.cols) o[64 * i] = v[i];
+        }
+      }
   }
   zero_rest<F32, VEC>(p);
 }

@@ -122,6 +122,20 @@ def test_gather_and_its_gradient(T, K, E, C, dtype):
     assert bool(((dx.cpu().double() - want).abs() <= mag * K * HALF[torch.float32] + want.abs() * HALF[dtype] * 1.01).all())
 
 
+@pytest.mark.parametrize("C", [64, 61])
+def test_gather_moves_every_bit_pattern(C):
+    """Subnormal values, infinities and NaN of any payload as they are, in both types."""
+    T = (65536 + C - 1) // C
+    routes = B.sort_routes(torch.arange(T, dtype=torch.int32).remainder(7)[:, None].cuda(), 7)
+    order = routes["sorted"].long()
+    x = torch.arange(T * C, dtype=torch.int32).to(torch.int16).view(T, C).cuda()
+    assert torch.equal(B.gather_rows(x, routes), x[order])
+    y = torch.randint(-(1 << 31), (1 << 31) - 1, (T, C), generator=gen(C)).to(torch.int32)
+    y[0, :4] = torch.tensor([1, 0x7F800001, -1, 0x00400000])
+    y = y.cuda().view(torch.float32)
+    assert torch.equal(B.gather_rows(y, routes).view(torch.int32), y.view(torch.int32)[order])
+
+
 @pytest.mark.parametrize("out_dtype", TYPES)
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T,K,E,C", SHAPES)
