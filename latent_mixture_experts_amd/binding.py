@@ -367,6 +367,13 @@ def _empty(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """_empty on the device of like (new_empty: a sixth less of a call's host time than the device by name)."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    return _empty(shape, dtype, like.device, stream)
+
+
 def _hold(stream, *tensors) -> None:
     """Memory of the call's tensors is not handed out again before the given
     stream has done the call, also when the caller drops them right after it."""
@@ -480,18 +487,26 @@ def fp8_grouped(x: torch.Tensor, x_scales: torch.Tensor, offsets: torch.Tensor, 
 _NIBBLES, _E8M0 = (torch.uint8,), (torch.uint8, torch.float8_e8m0fnu)
 
 
+def _result(like: torch.Tensor, out, rows: int, n: int, dtype, dev: torch.device, stream) -> torch.Tensor:
+    """_out, by _new."""
+    if out is None and stream is None and dtype in _FLOATS:
+        return like.new_empty((rows, n), dtype=dtype)
+    return _out(out, rows, n, dtype, dev, stream)
+
+
 def _fp4_quantize(what: str, x: torch.Tensor, cols: int, codes, scales, stream):
     dev = _device(x)
     rows = x.shape[0]
     _int32(rows | cols)
     _check("x", x, dev, _ANY_FLOAT, (rows, x.shape[1]), pitched=True)
-    _need(cols % 32 == 0, f"x: needs a width in groups of 32, got {cols}")
+    if cols % 32:
+        raise ValueError(f"x: needs a width in groups of 32, got {cols}")
     if codes is None:
-        codes = _empty((rows, cols // 2), torch.uint8, dev, stream)
+        codes = _new(x, (rows, cols // 2), torch.uint8, stream)
     else:
         _check("codes", codes, dev, _NIBBLES, (rows, cols // 2))
     if scales is None:
-        scales = _empty((rows, cols // 32), torch.uint8, dev, stream)
+        scales = _new(x, (rows, cols // 32), torch.uint8, stream)
     else:
         _check("scales", scales, dev, _E8M0, (rows, cols // 32))
     _hold(stream, x, codes, scales)
@@ -525,7 +540,7 @@ def fp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, out_dtype=torch.bf
     _int32(rows | cols)
     _check("codes", codes, dev, _NIBBLES, (rows, cols // 2))
     _check("scales", scales, dev, _E8M0, (rows, cols // 32))
-    out = _out(out, rows, cols, out_dtype, dev, stream)
+    out = _result(codes, out, rows, cols, out_dtype, dev, stream)
     _hold(stream, codes, scales, out)
     _run("moe_fp4_dequantize", dev, stream, rows, cols, codes.data_ptr(), scales.data_ptr(), out.data_ptr(),
          _pitch(out), _FLOATS[out.dtype])
@@ -546,7 +561,7 @@ def fp4_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     _check("x_scales", x_scales, dev, _E8M0, (T, K // 32))
     _check("w", w, dev, _NIBBLES, (N, half))
     _check("w_scales", w_scales, dev, _E8M0, (N, K // 32))
-    out = _out(out, T, N, out_dtype, dev, stream)
+    out = _result(x, out, T, N, out_dtype, dev, stream)
     _hold(stream, x, x_scales, w, w_scales, out)
     _run("moe_fp4_linear", dev, stream, T, N, K, x.data_ptr(), _pitch(x), x_scales.data_ptr(), w.data_ptr(),
          w_scales.data_ptr(), out.data_ptr(), _pitch(out), _FLOATS[out.dtype])
@@ -574,7 +589,7 @@ def fp4_grouped(x: torch.Tensor, x_scales: torch.Tensor, offsets: torch.Tensor, 
     _check("w_scales", w_scales, dev, _E8M0, (E, N, K // 32))
     if row_index is not None:
         _check("row_index", row_index, dev, _I32, (rows,))
-    out = _out(out, rows, N, out_dtype, dev, stream)
+    out = _result(x, out, rows, N, out_dtype, dev, stream)
     _hold(stream, x, x_scales, offsets, w, w_scales, row_index, out)
     _run("moe_fp4_grouped", dev, stream, rows, E, N, K, offsets.data_ptr(), _ptr(row_index), index_div,
          x_rows, x.data_ptr(), _pitch(x), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
@@ -600,26 +615,31 @@ def sort_routes(ids: torch.Tensor, n_experts: int, first: int = 0, ws=None, stre
     _need(n_experts >= 0, "n_experts: negative")
     if ws is None:
         n = sort_workspace_bytes(T, n_experts, K)
-        ws = _empty(n, torch.uint8, dev, stream) if n else None
+        ws = _new(ids, n, torch.uint8, stream) if n else None
     else:
         _check("ws", ws, dev, (torch.uint8,), (ws.numel(),))
-    offsets = _empty(n_experts + 1, torch.int32, dev, stream)
-    order = _empty(T * K, torch.int32, dev, stream)
-    positions = _empty((T, K), torch.int32, dev, stream)
+    offsets = _new(ids, n_experts + 1, torch.int32, stream)
+    order = _new(ids, T * K, torch.int32, stream)
+    positions = _new(ids, (T, K), torch.int32, stream)
     _hold(stream, ids, ws)
     _run("moe_sort_routes", dev, stream, T, n_experts, K, ids.data_ptr(), first, offsets.data_ptr(),
          order.data_ptr(), positions.data_ptr(), _ptr(ws), ws.numel() if ws is not None else 0)
     return dict(offsets=offsets, sorted=order, positions=positions)
 
 
+def _int32_tensor(name: str, t: torch.Tensor, dev: torch.device, dims: int) -> torch.Tensor:
+    if t.dtype != torch.int32 or t.device != dev or t.dim() != dims or not t.is_contiguous():
+        raise ValueError(f"{name}: needs a dense int32 tensor of {dims} dimension(s) on {dev}, got {list(t.shape)} "
+                         f"{t.dtype} on {t.device}, strides {t.stride()}")
+    return t
+
+
 def _positions(routes: dict, dev: torch.device, zero_rest: bool):
     """(positions, device address of the count of rows that are taken, or None; the tensor that holds it)."""
-    positions, offsets = routes["positions"], routes["offsets"]
-    _need(positions.dim() == 2, "positions: needs two dimensions")
-    _check("positions", positions, dev, _I32, tuple(positions.shape))
+    positions = _int32_tensor("positions", routes["positions"], dev, 2)
     if not zero_rest:
         return positions, None, None
-    _check("offsets", offsets, dev, _I32, (offsets.numel(),))
+    offsets = _int32_tensor("offsets", routes["offsets"], dev, 1)
     _need(offsets.numel() > 0, "offsets: empty")
     return positions, offsets.data_ptr() + 4 * (offsets.numel() - 1), offsets
 
@@ -664,7 +684,7 @@ def _gather_rows(x, routes, out, zero_rest, stream):
     _int32(T | K | rows | cols)
     _check("x", x, dev, _ANY_FLOAT, (T, cols), pitched=True)
     if out is None:
-        out = _empty((rows, cols), x.dtype, dev, stream)
+        out = _new(x, (rows, cols), x.dtype, stream)
     else:
         _check("out", out, dev, (x.dtype,), (rows, cols), pitched=True)
     _hold(stream, x, positions, offsets, out)
@@ -721,7 +741,7 @@ def _combine_rows(rows, routes, w, out_dtype, out, stream):
     _check("rows", rows, dev, _ANY_FLOAT, (n, cols), pitched=True)
     if w is not None:
         _check("w", w, dev, _F32, (T, K))
-    out = _out(out, T, cols, rows.dtype if out_dtype is None else out_dtype, dev, stream)
+    out = _result(rows, out, T, cols, rows.dtype if out_dtype is None else out_dtype, dev, stream)
     _hold(stream, rows, positions, w, out)
     _run("moe_combine_rows", dev, stream, T, K, n, cols, rows.data_ptr(), _pitch(rows), _FLOATS[rows.dtype],
          positions.data_ptr(), _ptr(w), out.data_ptr(), _pitch(out), _FLOATS[out.dtype])
@@ -747,8 +767,8 @@ def combine_rows_backward(grad_out: torch.Tensor, rows: torch.Tensor, routes: di
         _need(want_rows, "grad_rows: given, but not wanted")
         _check("grad_rows", grad_rows, dev, (rows.dtype,), (n, cols), pitched=True)
     elif want_rows:
-        grad_rows = _empty((n, cols), rows.dtype, dev, stream)
-    grad_w = _empty((T, K), torch.float32, dev, stream) if want_w else None
+        grad_rows = _new(rows, (n, cols), rows.dtype, stream)
+    grad_w = _new(rows, (T, K), torch.float32, stream) if want_w else None
     if not (want_rows or want_w):
         return None, None
     _hold(stream, grad_out, rows, positions, offsets, w, grad_rows)
