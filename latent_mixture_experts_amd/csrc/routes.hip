@@ -36,8 +36,8 @@ namespace {
 // places, its workgroups each adding up the chunks before their own (up to
 // kFewRoutes, where that is little, in runs of one step), or after a launch that
 // turns the counts into places first (longer runs: fewer counts to write and
-// read). All latency: 64 routes 4.0 us, 3000 8, 32768 8.5 (runs of two steps 11.3),
-// 262136 13.3; 8 million 125 us (runs of one step 167).
+// read). All latency: 64 routes 3.9 us, 4096 7.9, 32768 8.6 (runs of two steps 11.3),
+// 262136 13.3; 8 million 103 us (runs of two steps 125, of one 167).
 constexpr int kSortWaves = 16, kOneGroup = 2560, kFewRoutes = 1 << 18, kExperts = 256;
 constexpr int kShortRun = 64, kLongRun = 256;
 __host__ __device__ constexpr int chunk_of(int R) { return kSortWaves * (R <= kFewRoutes ? kShortRun : kLongRun); }
@@ -298,7 +298,7 @@ struct TokenRoutes {
   float w[kMaxK];
 };
 template <bool WEIGHTS>
-__device__ __forceinline__ TokenRoutes routes_of(const RouteRows& p, int64_t t, int lane) {
+__device__ __forceinline__ TokenRoutes routes_of(const RouteRows& p, int t, int lane) {
   const int v = lane < p.K ? p.positions[t * p.K + lane] : -1, mine = v >= 0 && v < p.rows ? v : -1;
   const float w = WEIGHTS && p.w && lane < p.K ? p.w[t * p.K + lane] : 1.0f;
   TokenRoutes r;
@@ -312,19 +312,17 @@ __device__ __forceinline__ TokenRoutes routes_of(const RouteRows& p, int64_t t, 
 
 // A workgroup's four wavefronts take 2^log spans of 4 >> log tokens, and
 // neighbouring workgroups the same tokens' next spans (nq workgroups to a set of
-// tokens), so that a row is read as a whole at about one time (combine, 4096 tokens
-// of 8 rows of 4096 bf16: by spans first 92 us).
+// tokens), so that a row is read as a whole at about one time.
 struct Walk {
-  int64_t token, step;  // first token of this wavefront, and to its next
-  int span;             // of `spans`, turned by the token; -1: none
-  int spans;
+  int token, step;  // first token of this wavefront (T: none), and to its next
+  int span, spans;  // its span before the token's turn, of so many
 };
 __device__ __forceinline__ Walk walk_of(const RouteRows& p, int wave, int log, int nq) {
   Walk w;
   w.spans = (p.cols + kSpan - 1) / kSpan;
   const int set = static_cast<int>(blockIdx.x) / nq, q = static_cast<int>(blockIdx.x) - set * nq;
-  w.token = static_cast<int64_t>(set) * (4 >> log) + (wave >> log);
-  w.step = static_cast<int64_t>(gridDim.x / nq) * (4 >> log);
+  w.token = set * (4 >> log) + (wave >> log);
+  w.step = static_cast<int>(gridDim.x) / nq * (4 >> log);
   w.span = (q << log) + (wave & ((1 << log) - 1));
   if (w.span >= w.spans) w.token = p.T;
   return w;
@@ -339,9 +337,9 @@ __global__ __launch_bounds__(256) void gather_rows_kernel(RouteRows p, int log, 
   Bits* out = static_cast<Bits*>(p.out);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Walk walk = walk_of(p, wave, log, nq);
-  for (int64_t t = walk.token; t < p.T; t += walk.step) {
+  for (int t = walk.token; t < p.T; t += walk.step) {
     const TokenRoutes r = routes_of<false>(p, t, lane);
-    const int c = span_column<VEC>(static_cast<int>((walk.span + t) % walk.spans), lane);
+    const int c = span_column<VEC>((walk.span + t) % walk.spans, lane);
     if (c >= p.cols) continue;
     uint4 piece[kWords];
     Bits v[8];
@@ -373,9 +371,9 @@ template <bool XF32, bool OF32, bool VEC>
 __global__ __launch_bounds__(256) void combine_rows_kernel(RouteRows p, int log, int nq) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Walk walk = walk_of(p, wave, log, nq);
-  for (int64_t t = walk.token; t < p.T; t += walk.step) {
+  for (int t = walk.token; t < p.T; t += walk.step) {
     const TokenRoutes r = routes_of<true>(p, t, lane);
-    const int c = span_column<VEC>(static_cast<int>((walk.span + t) % walk.spans), lane);
+    const int c = span_column<VEC>((walk.span + t) % walk.spans, lane);
     if (c >= p.cols) continue;
     float v[kMaxK][8], sum[8] = {};
 #pragma unroll
@@ -399,11 +397,11 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(RouteRows p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr int kTokens = 4 / WPT;
   const int spans = (p.cols + kSpan - 1) / kSpan;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + wave / WPT; t < p.T; t += static_cast<int64_t>(gridDim.x) * kTokens) {
+  for (int t = static_cast<int>(blockIdx.x) * kTokens + wave / WPT; t < p.T; t += static_cast<int>(gridDim.x) * kTokens) {
     const TokenRoutes r = routes_of<true>(p, t, lane);
     float dot[kMaxK] = {};
     for (int s = wave % WPT; s < spans; s += WPT) {
-      const int c = span_column<VEC>(static_cast<int>((s + t) % spans), lane);
+      const int c = span_column<VEC>((s + t) % spans, lane);
       if (c >= p.cols) continue;
       float g[8], v[kMaxK][8];
       load_span<GF32, VEC>(p.grad, t * p.ldg, c, p.cols, g);
