@@ -188,7 +188,7 @@ __global__ __launch_bounds__(64 * WT * WW * KG) void fp4_tile_kernel(Fp4Gemm p, 
   // wavefronts may have one fewer
   constexpr int kXOps = (BM / 8 + kGroup - 1) / kGroup, kXLeast = BM / 8 / kGroup, kWOps = BN / 8 / kGroup;
   constexpr int kOps = kXOps + kWOps, kLeast = (kXLeast + kWOps) * (WIDE ? 1 : 2);
-  static_assert(!EARLY || (R == 2 && KG == 1 && WIDE), "two stages held");
+  static_assert(!EARLY || (R == 2 && KG == 1), "two stages held");
   static_assert(kWOps * 8 * kGroup == BN && kXLeast > 0, "whole copies");
   static_assert(R >= 2 && R <= 4 && (R - 2) * kLeast < 64, "vmcnt field; scale sets land in time");
   constexpr int kXSlot = KG * BM * kRowBytes, kWSlot = KG * BN * kRowBytes;  // bytes of a stage
@@ -391,7 +391,7 @@ __global__ __launch_bounds__(64 * WT * WW * KG) void fp4_tile_kernel(Fp4Gemm p, 
     __syncthreads();
     // the copies of stage st + 1 have landed, in every wavefront
     auto meet = [&](int st, int slot) __attribute__((always_inline)) {
-      wait_vm_lds<EARLY ? kWOps : (R - 2) * kLeast>();
+      wait_vm_lds<EARLY ? kWOps * (WIDE ? 1 : 2) : (R - 2) * kLeast>();
       __syncthreads();
       if constexpr (!kPairs) issue_set(st + R, slot);
       // (of pairs: set j is read until stage 2j + 1's meeting and takes set j + 2
@@ -632,12 +632,13 @@ hipError_t launch_tile_as(const Fp4Gemm& g, hipStream_t st) {
     MOE_LAUNCH((fp4_tile_kernel<WT, WW, FT, FW, R, KG, SCALES, EARLY, false>), dim3(grid), block, 0, st, g, nrt, nct, chunk);
   return hipGetLastError();
 }
-// RB: stages held with scales by bytes, which take more LDS.
+// RB: stages held with scales by bytes, which take more LDS (two of them: EARLY, 64
+// experts of 128 rows x 4096 x 2880 188 -> 174 us).
 template <int WT, int WW, int FT, int FW, int R, int KG, int RB = R, bool EARLY = false>
 hipError_t launch_tile(const Fp4Gemm& g, hipStream_t st) {
   if (g.scales == kBy16) return launch_tile_as<WT, WW, FT, FW, R, KG, kBy16, EARLY>(g, st);
   if (g.scales == kBy4) return launch_tile_as<WT, WW, FT, FW, R, KG, kBy4, EARLY>(g, st);
-  return launch_tile_as<WT, WW, FT, FW, RB, KG, kBy1>(g, st);
+  return launch_tile_as<WT, WW, FT, FW, RB, KG, kBy1, RB == 2>(g, st);
 }
 
 // The tiles: rows, weight rows, and what one takes in ns: start and end, and per

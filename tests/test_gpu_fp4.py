@@ -317,7 +317,8 @@ def test_grouped(counts, N, K, dtype):
 
 
 @pytest.mark.parametrize("T,E,K_,N,K", [(1, 16, 8, 100, 512), (9, 8, 3, 64, 96), (61, 32, 4, 200, 1024), (300, 8, 2, 256, 288),
-                                       (1000, 4, 2, 130, 512)])
+                                       (1000, 4, 2, 130, 512), (2000, 4, 2, 4096, 512), (1000, 8, 8, 2048, 640),
+                                       (700, 16, 8, 3000, 416)])
 def test_grouped_gathers_tokens(T, E, K_, N, K):
     g = gen(T)
     x, xs, w, ws = operands(T, N, K, g, E)
@@ -408,6 +409,23 @@ def test_other_stream_and_dropped_tensors():
     ref, ref_s = R.quantize(x)
     assert torch.equal(back.cpu().double(), R.values(ref, ref_s))
     del junk
+
+
+def test_two_streams_at_once():
+    """Calls that share weights and overlap in time, each on a stream of its own."""
+    a, b = operands(300, 2048, 1024, gen(20)), operands(1000, 2048, 1024, gen(21))
+    w, ws = a[2].cuda(), a[3].cuda()
+    dev = [[t.cuda() for t in o[:2]] for o in (a, b)]
+    want = [B.fp4_linear(x, xs, w, ws, torch.float32) for x, xs in dev]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            got[i].append(B.fp4_linear(*dev[i], w, ws, torch.float32, stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
 
 
 def test_captured_and_replayed():

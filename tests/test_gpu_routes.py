@@ -402,6 +402,26 @@ def test_gradients_are_refused_in_a_capture():
             assert torch.equal(dx, B.gather_rows_backward(d2, routes))
 
 
+def test_the_same_bits_every_time_and_on_two_streams():
+    g = gen(16)
+    T, K, E, C = 900, 8, 64, 1030
+    ids, x, w = random_ids(T, K, E, g).cuda(), torch.randn((T, C), generator=g).cuda(), torch.rand((T, K), generator=g).cuda()
+
+    def step(stream=None):
+        routes = B.sort_routes(ids, E, stream=stream)
+        rows = B.gather_rows(x, routes, zero_rest=True, stream=stream)
+        out = B.combine_rows(rows, routes, w, stream=stream)
+        return (*routes.values(), rows, out, *B.combine_rows_backward(out, rows, routes, w, zero_rest=True, stream=stream))
+
+    want = step()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [step(s) for _ in range(8) for s in streams]
+    torch.cuda.synchronize()
+    for r in got:
+        assert all(torch.equal(a, b) for a, b in zip(r, want))
+
+
 def test_sort_captured_and_replayed():
     g = gen(14)
     for T in (5, 3000, 20000):
