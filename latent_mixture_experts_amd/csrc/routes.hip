@@ -227,16 +227,21 @@ __global__ __launch_bounds__(1024) void sort_place_kernel(SortRoutes s, int G) {
 // A wavefront takes spans of kSpan columns of a token, eight values a lane: eight
 // neighbours where rows allow it (VEC), else 64 apart. Tokens start at different
 // spans: their rows lie a power of two apart as a rule, and wavefronts that walk
-// them in step meet on the same memory channels. Loads pass the caches by, which
-// leaves those to the rows on their way out (4096 tokens of 8 rows of 4096 bf16, in
-// one stream: sort, gather and its gradient 150 -> 121 us, combine and its gradient
-// 185 -> 162; stores that do so: 127 and 161, both: 125 and 168).
+// them in step meet on the same memory channels. Stores of whole pieces pass the
+// caches by, which leaves those to the rows that are read (4096 tokens of 8 rows of
+// 4096 bf16, in one stream: sort, gather and its gradient 149 -> 124 us, combine and
+// its gradient 183 -> 160; loads that do so instead: 130 and 180; 8352 tokens of 7 rows
+// of 376 fp32, combine and its gradient: 62 -> 56, loads 69).
 constexpr int kMaxK = 8, kSpan = 512;
+
+__device__ __forceinline__ void store16(void* p, uint4 v) {
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), static_cast<u32x4*>(p));
+}
 
 template <bool F32, bool VEC>
 __device__ __forceinline__ void load_span(const void* x, int64_t row, int c, int cols, float v[8]) {
   if constexpr (VEC) {
-    load8<F32, true>(x, row + c, v);
+    load8<F32>(x, row + c, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -250,14 +255,14 @@ template <bool F32, bool VEC>
 __device__ __forceinline__ void store_span(void* x, int64_t row, int c, int cols, const float v[8]) {
   if constexpr (VEC) {
     if constexpr (F32) {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(x) + row + c);
-      o[0] = float4{v[0], v[1], v[2], v[3]};
-      o[1] = float4{v[4], v[5], v[6], v[7]};
+      float* o = static_cast<float*>(x) + row + c;
+      store16(o, __builtin_bit_cast(uint4, f32x4{v[0], v[1], v[2], v[3]}));
+      store16(o + 4, __builtin_bit_cast(uint4, f32x4{v[4], v[5], v[6], v[7]}));
     } else {
       bf16x8 b;
 #pragma unroll
       for (int i = 0; i < 8; ++i) b[i] = static_cast<__bf16>(v[i]);
-      *reinterpret_cast<bf16x8*>(static_cast<uint16_t*>(x) + row + c) = b;
+      store16(static_cast<uint16_t*>(x) + row + c, __builtin_bit_cast(uint4, b));
     }
   } else {
 #pragma unroll
@@ -345,7 +350,7 @@ __global__ __launch_bounds__(256) void gather_rows_kernel(RouteRows p, int log, 
     Bits v[8];
     if constexpr (VEC) {
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) piece[i] = load16<true>(x + t * p.ldx + c + i * (16 / sizeof(Bits)));
+      for (int i = 0; i < kWords; ++i) piece[i] = load16<false>(x + t * p.ldx + c + i * (16 / sizeof(Bits)));
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = c + 64 * i < p.cols ? x[t * p.ldx + c + 64 * i] : 0;
@@ -356,7 +361,7 @@ __global__ __launch_bounds__(256) void gather_rows_kernel(RouteRows p, int log, 
         Bits* o = out + r.at[k] * p.ldo + c;
         if constexpr (VEC) {
 #pragma unroll
-          for (int i = 0; i < kWords; ++i) *reinterpret_cast<uint4*>(o + i * (16 / sizeof(Bits))) = piece[i];
+          for (int i = 0; i < kWords; ++i) store16(o + i * (16 / sizeof(Bits)), piece[i]);
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
