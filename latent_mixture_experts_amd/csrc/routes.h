@@ -19,7 +19,7 @@ struct SortRoutes {
   int32_t* counts;  // workspace
   int R, E, first;
 };
-size_t sort_workspace(int R, int E);
+size_t sort_workspace(int R);
 hipError_t launch_sort_routes(const SortRoutes& s, hipStream_t st);
 
 // The rows of T tokens' K routes: row positions[t * K + k] of `rows` rows; a

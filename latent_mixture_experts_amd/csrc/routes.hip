@@ -477,7 +477,7 @@ struct Spans {
 
 }  // namespace
 
-size_t sort_workspace(int R, int) {
+size_t sort_workspace(int R) {
   if (R <= kOneGroup) return 0;
   return static_cast<size_t>((R + chunk_of(R) - 1) / chunk_of(R) + 1) * kExperts * sizeof(int32_t);
 }

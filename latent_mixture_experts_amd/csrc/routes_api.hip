@@ -38,7 +38,7 @@ extern "C" {
 
 size_t moe_sort_workspace_bytes(int32_t T, int32_t n_experts, int32_t top_k) {
   if (check_routes(T, top_k) != MOE_OK || n_experts <= 0 || n_experts > kMaxExperts) return 0;
-  return sort_workspace(T * top_k, n_experts);
+  return sort_workspace(T * top_k);
 }
 
 int moe_sort_routes_validate(int32_t T, int32_t n_experts, int32_t top_k, const int32_t* topk_ids,

@@ -241,7 +241,12 @@ def test_strides(C, dtype):
         a = B.combine_rows_backward(out[:, shift:shift + C], hold[:, shift:shift + C], routes, w, zero_rest=True,
                                     grad_rows=drows[:, shift:shift + C])
         b = B.combine_rows_backward(out[:, shift:shift + C].contiguous(), want, routes, w, zero_rest=True)
-        assert torch.equal(a[0], b[0]) and torch.allclose(a[1], b[1], rtol=1e-4, atol=1e-3)
+        # (dots in another order: each within C + 16 roundings of its terms' sizes)
+        at = routes["positions"].long()
+        mine = torch.where((at >= 0)[:, :, None], want.double()[at.clamp(min=0)], torch.zeros((), dtype=torch.float64, device="cuda"))
+        mag = (mine.abs() * out[:, shift:shift + C].double().abs()[:, None, :]).sum(2)
+        assert torch.equal(a[0], b[0])
+        assert bool(((a[1].double() - b[1].double()).abs() <= 2 * (C + 16) * HALF[torch.float32] * mag).all())
         assert (drows[:, :shift] == -5).all() and (drows[:, shift + C:] == -5).all()
 
 
