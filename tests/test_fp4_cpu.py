@@ -2,6 +2,8 @@
 the argument checks, and the oracle against definitions of its own."""
 from __future__ import annotations
 
+import types
+
 import pytest
 import torch
 
@@ -206,6 +208,57 @@ def test_binding_refuses_host_tensors():
                  lambda: B.combine_rows(x, routes), lambda: B.combine_rows_backward(x, x, routes),
                  lambda: B.gather_rows(x.requires_grad_(), routes)):
         with pytest.raises(ValueError, match="GPU"):
+            call()
+
+
+def test_a_given_stream_holds_every_tensor_of_the_call(monkeypatch):
+    """What a call on a stream of its own reads or writes is recorded on that stream before anything is
+    enqueued; a stream of another device is refused before that."""
+    held, enqueued = set(), []
+    monkeypatch.setattr(B, "_device", lambda t: t.device)
+    monkeypatch.setattr(B, "_empty", lambda shape, dtype, dev, stream: torch.empty(shape, dtype=dtype))
+    monkeypatch.setattr(B, "_run", lambda *a: enqueued.append(set(held)))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: held.add((t.data_ptr(), id(s))))
+    mine = types.SimpleNamespace(device=torch.device("cpu"), cuda_stream=0)
+    other = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+
+    def run(fn, reads, *args, **named):
+        held.clear()
+        with pytest.raises(ValueError, match="stream"):
+            fn(*args, **named, stream=other)
+        assert not held, fn.__name__
+        for stream in (mine, None):
+            held.clear()
+            fn(*args, **named, stream=stream)
+            want = {(t.data_ptr(), id(stream)) for t in reads} if stream else set()
+            assert want <= enqueued[-1] and (stream or not enqueued[-1]), (fn.__name__, stream)
+
+    u8, i32 = torch.uint8, torch.int32
+    x = torch.zeros((4, 256))
+    c, s = torch.zeros((4, 128), dtype=u8), torch.zeros((4, 8), dtype=u8)
+    run(B.fp4_quantize, (x, c, s), x, c, s)
+    run(B.fp4_quantize, (x,), x)
+    run(B.fp4_swiglu, (x,), x)
+    run(B.fp4_dequantize, (c, s, x), c, s, out=x)
+    run(B.fp4_dequantize, (c, s), c, s)
+    w, ws, off = torch.zeros((2, 16, 128), dtype=u8), torch.zeros((2, 16, 8), dtype=u8), torch.zeros(3, dtype=i32)
+    out, idx = torch.zeros((6, 16)), torch.zeros(6, dtype=i32)
+    run(B.fp4_linear, (c, s, w[0], ws[0], out), c, s, w[0], ws[0], out=out[:4])
+    run(B.fp4_grouped, (c, s, off, w, ws, idx, out), c, s, off, w, ws, row_index=idx, out=out)
+    ids, sw = torch.zeros((900, 4), dtype=i32), torch.zeros(1 << 16, dtype=u8)
+    run(B.sort_routes, (ids, sw), ids, 8, ws=sw)
+    routes = dict(offsets=off, sorted=torch.zeros(8, dtype=i32), positions=torch.zeros((4, 2), dtype=i32))
+    rows, wt = torch.zeros((8, 256)), torch.zeros((4, 2))
+    run(B.gather_rows, (x, off, routes["positions"], rows), x, routes, out=rows, zero_rest=True)
+    run(B.gather_rows_backward, (rows, routes["positions"], x), rows, routes, out=x)
+    run(B.combine_rows, (rows, routes["positions"], wt, x), rows, routes, wt, out=x)
+    run(B.combine_rows_backward, (x, rows, routes["positions"], off, wt), x, rows, routes, wt, zero_rest=True)
+    run(B.combine_rows_backward, (x, rows, routes["positions"], wt, rows), x, rows, routes, wt, grad_rows=torch.zeros((8, 256)))
+
+
+def test_sizes_past_32_bits_are_refused():
+    for call in (lambda: B.sort_workspace_bytes(2 ** 32 + 4096, 16, 4), lambda: B.sort_workspace_bytes(4, 2 ** 40, 4)):
+        with pytest.raises(ValueError, match="32-bit"):
             call()
 
 
