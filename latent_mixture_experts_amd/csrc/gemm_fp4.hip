@@ -46,7 +46,8 @@ __device__ __forceinline__ f32x4 mfma_fp4(uint4 a, uint32_t sa, uint4 b, uint32_
 // A wavefront takes 16 weight rows x up to 16 rows over a run of K's chunks of
 // 512 values; KS wavefronts of a workgroup split K and are joined through LDS
 // in order, and the workgroup's 8 / KS such teams take neighbouring weight
-// rows. Dense, at most 16 rows. Grid: weight row tiles.
+// rows. Dense products of at most 16 rows only: it reads neither offsets nor an
+// index, which one expert, too, may come with. Grid: weight row tiles.
 constexpr int kFW = 8;      // wavefronts
 constexpr int kChunk = 512; // values of a chunk: 256 bytes of codes, 16 scales
 
@@ -716,7 +717,7 @@ int best_tile(const Fp4Gemm& g) {
 // Per expert the tiles are level with it (8 routes of one token, N = 4096, K =
 // 4096: 18.9 / 16.4) or better (32 tokens' 163 experts 296 / 252).
 bool streams(const Fp4Gemm& g) {
-  return g.experts == 1 && g.rows <= 16 && static_cast<int64_t>(g.rows) * g.K <= (g.N <= 4096 ? 128 << 10 : 16 << 10);
+  return !g.offsets && g.rows <= 16 && static_cast<int64_t>(g.rows) * g.K <= (g.N <= 4096 ? 128 << 10 : 16 << 10);
 }
 
 }  // namespace

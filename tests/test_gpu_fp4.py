@@ -356,6 +356,50 @@ def test_grouped_bad_lists_stay_in_bounds(rows):
     check_grouped(out, x.cpu(), xs.cpu(), [0, 5, 5, 10, rows], w.cpu(), ws.cpu(), torch.float32, clamped)
 
 
+@pytest.mark.parametrize("N,K", [(64, 64), (256, 512), (100, 416), (4100, 1024), (4096, 1152)])
+@pytest.mark.parametrize("rows", [1, 7, 8, 16, 17, 40])
+def test_grouped_one_expert(rows, N, K):
+    """One expert is no dense product: its offsets may leave rows out, an index names its rows. Behind x's own rows
+    lie others with NaN scales."""
+    g = gen(rows + N + K)
+    div = 8
+    tokens = (rows + div - 1) // div
+    x, xs, w, ws = operands(tokens + rows, N, K, g, 1)
+    xs[tokens:] = 255
+    xd, xsd, wd, wsd = (t.cuda() for t in (x, xs, w, ws))
+    order = torch.randperm(rows, generator=g).to(torch.int32)
+    first, last = (2, rows - 3) if rows > 5 else (0, rows)
+    for a, b in ((0, rows), (first, last)):
+        off = torch.tensor([a, b], dtype=torch.int32)
+        out = torch.full((rows, N), -7.0, device="cuda")
+        B.fp4_grouped(xd[:tokens], xsd[:tokens], off.cuda(), wd, wsd, out=out, row_index=order.cuda(), index_div=div)
+        check_grouped(out, x, xs, off, w, ws, torch.float32, order.long() // div)
+        assert (out[:a] == -7).all() and (out[b:] == -7).all()
+    # rows that it does not take, without an index
+    x, xs = R.random_codes((rows, K // 2), g), R.random_scales((rows, K // 32), g)
+    out = torch.full((rows, N), -7.0, device="cuda")
+    B.fp4_grouped(x.cuda(), xs.cuda(), off.cuda(), wd, wsd, out=out)
+    check_grouped(out, x, xs, off, w, ws, torch.float32)
+    assert (out[:first] == -7).all() and (out[last:] == -7).all()
+
+
+def test_grouped_on_a_process_with_one_expert():
+    """Routes of which one expert is here: the rows behind the last one stay as they were."""
+    g = gen(12)
+    T, K_, N, K = 3, 4, 128, 256
+    x, xs, w, ws = operands(T, N, K, g, 1)
+    ids = torch.stack([torch.randperm(6, generator=g)[:K_] for _ in range(T)]).to(torch.int32)
+    ids[0, 0] = 5 if not (ids[0] == 5).any() else ids[0, 0]
+    routes = B.sort_routes(ids.cuda(), 1, 5)
+    taken = int(routes["offsets"][1])
+    assert 0 < taken < T * K_
+    out = torch.full((T * K_, N), -7.0, device="cuda")
+    B.fp4_grouped(x.cuda(), xs.cuda(), routes["offsets"], w.cuda(), ws.cuda(), out=out, row_index=routes["sorted"],
+                  index_div=K_)
+    check_grouped(out, x, xs, routes["offsets"].cpu(), w, ws, torch.float32, routes["sorted"].cpu().long() // K_)
+    assert (out[taken:] == -7).all()
+
+
 def test_grouped_offsets_past_32_bits():
     """Weights of more than 4 GiB: the last expert's."""
     E, N, K = 9, 32768, 32768
