@@ -153,6 +153,14 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+def _written(*given) -> None:
+    """Counts a write of the caller's tensors (None: not given), as torch's own calls
+    do: a backward pass that saved them before this call refuses to run on what they hold now."""
+    given = [t for t in given if isinstance(t, torch.Tensor)]
+    if given:
+        torch.autograd.graph.increment_version(given)
+
+
 def _stream(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -204,6 +212,7 @@ def route(d: MoeDims, x: torch.Tensor, router: torch.Tensor, ws: torch.Tensor,
                          _ptr(out["logits"]), _ptr(ws), ws.numel(), _stream(stream))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_route")
+    _written(ws)
     return out
 
 
@@ -222,6 +231,7 @@ def latent_forward(d: MoeDims, x: torch.Tensor, weights: MoeWeights, out: torch.
                                             _ptr(out), _ptr(ws), ws.numel(), _stream(stream), arr)
     if rc != MOE_OK:
         raise MoeError(rc, "moe_latent_forward")
+    _written(out, ws)
     return out
 
 
@@ -236,6 +246,7 @@ def latent_forward_routed(d: MoeDims, x: torch.Tensor, ids: torch.Tensor, w: tor
                                          _stream(stream))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_latent_forward_routed")
+    _written(out, ws)
     return out
 
 
@@ -247,6 +258,7 @@ def latent_forward_persistent(d: MoeDims, x: torch.Tensor, weights: MoeWeights, 
                                              _ptr(out), _ptr(ws), ws.numel(), _stream(stream))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_latent_forward_persistent")
+    _written(out, ws)
     return out
 
 
@@ -259,6 +271,7 @@ def latent_forward_noalloc(d: MoeDims, x: torch.Tensor, weights: MoeWeights, out
                                           _ptr(out), _stream(stream))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_latent_forward_noalloc")
+    _written(out)
     return out
 
 
@@ -272,6 +285,7 @@ def block_forward(d: MoeDims, resid: torch.Tensor, pre_gain: torch.Tensor, post_
                                  _stream(stream))
     if rc != MOE_OK:
         raise MoeError(rc, "moe_block_forward")
+    _written(out, ws)
     return out
 
 
@@ -297,6 +311,7 @@ def workspace_view(d: MoeDims, T: int, ws: torch.Tensor, which: str, dtype, shap
 # torch.cuda.Stream). What they allocate then belongs to that stream, and what
 # they were given may be dropped once they return; order between the streams
 # (inputs written before, results read after, there or elsewhere) is the caller's.
+# Outputs that are given (out, codes, scales, grad_rows) count as written.
 # Only balance_loss, gather_rows and combine_rows are recorded for autograd; the
 # 8-bit and 4-bit calls have no gradient, and what they return requires none.
 TYPE_BF16, TYPE_F32 = 0, 1  # MOE_TYPE_*
@@ -396,6 +411,7 @@ def _quantize(what: str, x: torch.Tensor, cols: int, codes, scales, stream):
     rows = x.shape[0]
     _int32(rows | cols)
     _check("x", x, dev, _ANY_FLOAT, (rows, x.shape[1]), pitched=True)
+    given = codes, scales
     if codes is None:
         codes = _empty((rows, cols), torch.float8_e4m3fn, dev, stream)
     else:
@@ -407,6 +423,8 @@ def _quantize(what: str, x: torch.Tensor, cols: int, codes, scales, stream):
     _hold(stream, x, codes, scales)
     _run(what, dev, stream, rows, cols, x.data_ptr(), _pitch(x), _FLOATS[x.dtype], codes.data_ptr(),
          scales.data_ptr())
+    if given[0] is not None or given[1] is not None:
+        _written(*given)
     return codes, scales
 
 
@@ -447,11 +465,14 @@ def fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     _check("x_scales", x_scales, dev, _F32, (T, _blocks(K)))
     _check("w", w, dev, _CODES, (N, K))
     _check("w_scales", w_scales, dev, _F32, (_blocks(N), _blocks(K)))
+    given = out
     out = _out(out, T, N, out_dtype, dev, stream)
     _hold(stream, x, x_scales, w, w_scales, out)
     _run("moe_fp8_linear", dev, stream, T, N, K, x.data_ptr(), _pitch(x), x_scales.data_ptr(),
          w.data_ptr(), w_scales.data_ptr(), out.data_ptr(), _pitch(out),
          _FLOATS[out.dtype] | SUM_F32 if f32_sums else _FLOATS[out.dtype])
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -476,11 +497,14 @@ def fp8_grouped(x: torch.Tensor, x_scales: torch.Tensor, offsets: torch.Tensor, 
     _check("w_scales", w_scales, dev, _F32, (E, _blocks(N), _blocks(K)))
     if row_index is not None:
         _check("row_index", row_index, dev, _I32, (rows,))
+    given = out
     out = _out(out, rows, N, out_dtype, dev, stream)
     _hold(stream, x, x_scales, offsets, w, w_scales, row_index, out)
     _run("moe_fp8_grouped", dev, stream, rows, E, N, K, offsets.data_ptr(), _ptr(row_index), index_div,
          x_rows, x.data_ptr(), _pitch(x), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
          out.data_ptr(), _pitch(out), _FLOATS[out.dtype] | SUM_F32 if f32_sums else _FLOATS[out.dtype])
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -501,6 +525,7 @@ def _fp4_quantize(what: str, x: torch.Tensor, cols: int, codes, scales, stream):
     _check("x", x, dev, _ANY_FLOAT, (rows, x.shape[1]), pitched=True)
     if cols % 32:
         raise ValueError(f"x: needs a width in groups of 32, got {cols}")
+    given = codes, scales
     if codes is None:
         codes = _new(x, (rows, cols // 2), torch.uint8, stream)
     else:
@@ -512,6 +537,8 @@ def _fp4_quantize(what: str, x: torch.Tensor, cols: int, codes, scales, stream):
     _hold(stream, x, codes, scales)
     _run(what, dev, stream, rows, cols, x.data_ptr(), _pitch(x), _FLOATS[x.dtype], codes.data_ptr(),
          scales.data_ptr())
+    if given[0] is not None or given[1] is not None:
+        _written(*given)
     return codes, scales
 
 
@@ -540,10 +567,13 @@ def fp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, out_dtype=torch.bf
     _int32(rows | cols)
     _check("codes", codes, dev, _NIBBLES, (rows, cols // 2))
     _check("scales", scales, dev, _E8M0, (rows, cols // 32))
+    given = out
     out = _result(codes, out, rows, cols, out_dtype, dev, stream)
     _hold(stream, codes, scales, out)
     _run("moe_fp4_dequantize", dev, stream, rows, cols, codes.data_ptr(), scales.data_ptr(), out.data_ptr(),
          _pitch(out), _FLOATS[out.dtype])
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -561,10 +591,13 @@ def fp4_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
     _check("x_scales", x_scales, dev, _E8M0, (T, K // 32))
     _check("w", w, dev, _NIBBLES, (N, half))
     _check("w_scales", w_scales, dev, _E8M0, (N, K // 32))
+    given = out
     out = _result(x, out, T, N, out_dtype, dev, stream)
     _hold(stream, x, x_scales, w, w_scales, out)
     _run("moe_fp4_linear", dev, stream, T, N, K, x.data_ptr(), _pitch(x), x_scales.data_ptr(), w.data_ptr(),
          w_scales.data_ptr(), out.data_ptr(), _pitch(out), _FLOATS[out.dtype])
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -589,11 +622,14 @@ def fp4_grouped(x: torch.Tensor, x_scales: torch.Tensor, offsets: torch.Tensor, 
     _check("w_scales", w_scales, dev, _E8M0, (E, N, K // 32))
     if row_index is not None:
         _check("row_index", row_index, dev, _I32, (rows,))
+    given = out
     out = _result(x, out, rows, N, out_dtype, dev, stream)
     _hold(stream, x, x_scales, offsets, w, w_scales, row_index, out)
     _run("moe_fp4_grouped", dev, stream, rows, E, N, K, offsets.data_ptr(), _ptr(row_index), index_div,
          x_rows, x.data_ptr(), _pitch(x), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
          out.data_ptr(), _pitch(out), _FLOATS[out.dtype])
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -683,6 +719,7 @@ def _gather_rows(x, routes, out, zero_rest, stream):
     rows = T * K if out is None else out.shape[0]
     _int32(T | K | rows | cols)
     _check("x", x, dev, _ANY_FLOAT, (T, cols), pitched=True)
+    given = out
     if out is None:
         out = _new(x, (rows, cols), x.dtype, stream)
     else:
@@ -690,6 +727,8 @@ def _gather_rows(x, routes, out, zero_rest, stream):
     _hold(stream, x, positions, offsets, out)
     _run("moe_gather_rows", dev, stream, T, K, rows, cols, x.data_ptr(), _pitch(x), _FLOATS[x.dtype],
          positions.data_ptr(), taken, out.data_ptr(), _pitch(out))
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -741,10 +780,13 @@ def _combine_rows(rows, routes, w, out_dtype, out, stream):
     _check("rows", rows, dev, _ANY_FLOAT, (n, cols), pitched=True)
     if w is not None:
         _check("w", w, dev, _F32, (T, K))
+    given = out
     out = _result(rows, out, T, cols, rows.dtype if out_dtype is None else out_dtype, dev, stream)
     _hold(stream, rows, positions, w, out)
     _run("moe_combine_rows", dev, stream, T, K, n, cols, rows.data_ptr(), _pitch(rows), _FLOATS[rows.dtype],
          positions.data_ptr(), _ptr(w), out.data_ptr(), _pitch(out), _FLOATS[out.dtype])
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -763,6 +805,7 @@ def combine_rows_backward(grad_out: torch.Tensor, rows: torch.Tensor, routes: di
     _check("rows", rows, dev, _ANY_FLOAT, (n, cols), pitched=True)
     if w is not None:
         _check("w", w, dev, _F32, (T, K))
+    given = grad_rows
     if grad_rows is not None:
         _need(want_rows, "grad_rows: given, but not wanted")
         _check("grad_rows", grad_rows, dev, (rows.dtype,), (n, cols), pitched=True)
@@ -775,6 +818,8 @@ def combine_rows_backward(grad_out: torch.Tensor, rows: torch.Tensor, routes: di
     _run("moe_combine_rows_backward", dev, stream, T, K, n, cols, grad_out.data_ptr(), _pitch(grad_out),
          _FLOATS[grad_out.dtype], rows.data_ptr(), _pitch(rows), _FLOATS[rows.dtype], positions.data_ptr(), _ptr(w),
          taken, _ptr(grad_rows), _pitch(grad_rows) if want_rows else cols, _ptr(grad_w))
+    if given is not None:
+        _written(given)
     return grad_rows, grad_w
 
 
@@ -880,6 +925,7 @@ def balance_loss_backward(logits: torch.Tensor, ids: torch.Tensor, counts: torch
     if w is not None:
         _check("w", w, dev, _F32, (T, K))
         _check("grad_w", grad_w, dev, _F32, (T, K))
+    given = out
     if out is None:
         out = _empty((T, E), torch.float32, dev, stream)
     else:
@@ -887,6 +933,8 @@ def balance_loss_backward(logits: torch.Tensor, ids: torch.Tensor, counts: torch
     _hold(stream, logits, ids, counts, grad_losses, mask, w, grad_w, out)
     _run("moe_balance_loss_backward", dev, stream, T, E, K, logits.data_ptr(), ids.data_ptr(), _ptr(mask),
          counts.data_ptr(), grad_losses.data_ptr(), _ptr(w), _ptr(grad_w), out.data_ptr())
+    if given is not None:
+        _written(given)
     return out
 
 

@@ -462,3 +462,24 @@ def test_other_stream_and_dropped_tensors():
     assert torch.allclose(out.cpu(), x * n[:, None], rtol=1e-6)
     assert grads[0].shape == (12000, 64)
     del junk
+
+
+def test_rows_refilled_before_the_backward_pass_are_refused():
+    """Frozen 4-bit experts, a trained router, one buffer of rows for every micro-batch."""
+    g = gen(17)
+    T, K, E, C = 20, 2, 4, 64
+    routes = B.sort_routes(torch.stack([torch.randperm(E, generator=g)[:K] for _ in range(T)]).to(torch.int32).cuda(), E)
+    w = B.fp4_quantize(torch.randn((E * C, C), generator=g).cuda())
+    w = w[0].view(E, C, C // 2), w[1].view(E, C, C // 32)
+    xs = [B.fp4_quantize(torch.randn((T * K, C), generator=g).cuda()) for _ in range(2)]
+    buf = torch.empty((T * K, C), device="cuda")
+    weights = torch.rand((T, K), generator=g).cuda().requires_grad_()
+    B.fp4_grouped(*xs[0], routes["offsets"], *w, out=buf)
+    y = B.combine_rows(buf, routes, weights)
+    y.sum().backward(retain_graph=True)
+    _, dw = B.combine_rows_backward(torch.ones_like(y), buf, routes, weights.detach())
+    assert torch.equal(weights.grad, dw)
+    B.fp4_grouped(*xs[1], routes["offsets"], *w, out=buf)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    assert torch.equal(weights.grad, dw)
