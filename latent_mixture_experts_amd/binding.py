@@ -153,6 +153,12 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+def _writable(name: str, t) -> None:
+    """The calls have no gradient for what they write."""
+    if isinstance(t, torch.Tensor) and t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name}: is written and requires a gradient (pass {name}.detach())")
+
+
 def _written(*given) -> None:
     """Counts a write of the caller's tensors (None: not given), as torch's own calls
     do: a backward pass that saved them before this call refuses to run on what they hold now."""
@@ -221,6 +227,7 @@ def latent_forward(d: MoeDims, x: torch.Tensor, weights: MoeWeights, out: torch.
     """moe_latent_forward, or moe_latent_forward_timed when ``events`` holds
     2 * MOE_N_STAGES hipEvent_t handles (start, stop of each step; None
     entries are skipped)."""
+    _writable("out", out)
     T = x.shape[0]
     if events is None:
         rc = lib().moe_latent_forward(ctypes.byref(d), T, _ptr(x), ctypes.byref(weights),
@@ -240,6 +247,7 @@ def latent_forward_routed(d: MoeDims, x: torch.Tensor, ids: torch.Tensor, w: tor
                           stream=None) -> torch.Tensor:
     """moe_latent_forward_routed: the layer with the routing given (ids
     [T][K] int32, w [T][K] fp32, on the device)."""
+    _writable("out", out)
     T = x.shape[0]
     rc = lib().moe_latent_forward_routed(ctypes.byref(d), T, _ptr(x), _ptr(ids), _ptr(w),
                                          ctypes.byref(weights), _ptr(out), _ptr(ws), ws.numel(),
@@ -253,6 +261,7 @@ def latent_forward_routed(d: MoeDims, x: torch.Tensor, ids: torch.Tensor, w: tor
 def latent_forward_persistent(d: MoeDims, x: torch.Tensor, weights: MoeWeights, out: torch.Tensor,
                               ws: torch.Tensor, stream=None) -> torch.Tensor:
     """moe_latent_forward_persistent: the layer for one or two tokens in one launch."""
+    _writable("out", out)
     T = x.shape[0]
     rc = lib().moe_latent_forward_persistent(ctypes.byref(d), T, _ptr(x), ctypes.byref(weights),
                                              _ptr(out), _ptr(ws), ws.numel(), _stream(stream))
@@ -266,6 +275,7 @@ def latent_forward_noalloc(d: MoeDims, x: torch.Tensor, weights: MoeWeights, out
                            stream=None) -> torch.Tensor:
     """moe_latent_forward_noalloc: the layer with the library's own per-GPU
     scratch array as its workspace (no workspace argument)."""
+    _writable("out", out)
     T = x.shape[0]
     rc = lib().moe_latent_forward_noalloc(ctypes.byref(d), T, _ptr(x), ctypes.byref(weights),
                                           _ptr(out), _stream(stream))
@@ -279,6 +289,7 @@ def block_forward(d: MoeDims, resid: torch.Tensor, pre_gain: torch.Tensor, post_
                   block_eps: float, weights: MoeWeights, out: torch.Tensor, ws: torch.Tensor,
                   stream=None) -> torch.Tensor:
     """moe_block_forward: out = resid + post_norm(layer(pre_norm(resid)))."""
+    _writable("out", out)
     T = resid.shape[0]
     rc = lib().moe_block_forward(ctypes.byref(d), T, _ptr(resid), _ptr(pre_gain), _ptr(post_gain),
                                  block_eps, ctypes.byref(weights), _ptr(out), _ptr(ws), ws.numel(),
@@ -311,7 +322,8 @@ def workspace_view(d: MoeDims, T: int, ws: torch.Tensor, which: str, dtype, shap
 # torch.cuda.Stream). What they allocate then belongs to that stream, and what
 # they were given may be dropped once they return; order between the streams
 # (inputs written before, results read after, there or elsewhere) is the caller's.
-# Outputs that are given (out, codes, scales, grad_rows) count as written.
+# Outputs that are given (out, codes, scales, grad_rows) count as written; one that
+# requires a gradient is refused.
 # Only balance_loss, gather_rows and combine_rows are recorded for autograd; the
 # 8-bit and 4-bit calls have no gradient, and what they return requires none.
 TYPE_BF16, TYPE_F32 = 0, 1  # MOE_TYPE_*
@@ -415,10 +427,12 @@ def _quantize(what: str, x: torch.Tensor, cols: int, codes, scales, stream):
     if codes is None:
         codes = _empty((rows, cols), torch.float8_e4m3fn, dev, stream)
     else:
+        _writable("codes", codes)
         _check("codes", codes, dev, _CODES, (rows, cols))
     if scales is None:
         scales = _empty((rows, _blocks(cols)), torch.float32, dev, stream)
     else:
+        _writable("scales", scales)
         _check("scales", scales, dev, _F32, (rows, _blocks(cols)))
     _hold(stream, x, codes, scales)
     _run(what, dev, stream, rows, cols, x.data_ptr(), _pitch(x), _FLOATS[x.dtype], codes.data_ptr(),
@@ -447,6 +461,7 @@ def _out(out, rows: int, n: int, dtype, dev: torch.device, stream) -> torch.Tens
         if dtype not in _FLOATS:
             raise ValueError(f"out_dtype: bfloat16 or float32, got {dtype}")
         return _empty((rows, n), dtype, dev, stream)
+    _writable("out", out)
     _check("out", out, dev, _ANY_FLOAT, (rows, n), pitched=True)
     return out
 
@@ -529,10 +544,12 @@ def _fp4_quantize(what: str, x: torch.Tensor, cols: int, codes, scales, stream):
     if codes is None:
         codes = _new(x, (rows, cols // 2), torch.uint8, stream)
     else:
+        _writable("codes", codes)
         _check("codes", codes, dev, _NIBBLES, (rows, cols // 2))
     if scales is None:
         scales = _new(x, (rows, cols // 32), torch.uint8, stream)
     else:
+        _writable("scales", scales)
         _check("scales", scales, dev, _E8M0, (rows, cols // 32))
     _hold(stream, x, codes, scales)
     _run(what, dev, stream, rows, cols, x.data_ptr(), _pitch(x), _FLOATS[x.dtype], codes.data_ptr(),
@@ -723,6 +740,7 @@ def _gather_rows(x, routes, out, zero_rest, stream):
     if out is None:
         out = _new(x, (rows, cols), x.dtype, stream)
     else:
+        _writable("out", out)
         _check("out", out, dev, (x.dtype,), (rows, cols), pitched=True)
     _hold(stream, x, positions, offsets, out)
     _run("moe_gather_rows", dev, stream, T, K, rows, cols, x.data_ptr(), _pitch(x), _FLOATS[x.dtype],
@@ -808,6 +826,7 @@ def combine_rows_backward(grad_out: torch.Tensor, rows: torch.Tensor, routes: di
     given = grad_rows
     if grad_rows is not None:
         _need(want_rows, "grad_rows: given, but not wanted")
+        _writable("grad_rows", grad_rows)
         _check("grad_rows", grad_rows, dev, (rows.dtype,), (n, cols), pitched=True)
     elif want_rows:
         grad_rows = _new(rows, (n, cols), rows.dtype, stream)
@@ -929,6 +948,7 @@ def balance_loss_backward(logits: torch.Tensor, ids: torch.Tensor, counts: torch
     if out is None:
         out = _empty((T, E), torch.float32, dev, stream)
     else:
+        _writable("out", out)
         _check("out", out, dev, _F32, (T, E))
     _hold(stream, logits, ids, counts, grad_losses, mask, w, grad_w, out)
     _run("moe_balance_loss_backward", dev, stream, T, E, K, logits.data_ptr(), ids.data_ptr(), _ptr(mask),

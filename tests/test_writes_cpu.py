@@ -95,3 +95,22 @@ def test_rows_overwritten_before_the_backward_pass_are_refused(host):
     B.fp4_grouped(c, s, off, w, ws, out=buf)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.sum().backward()
+
+
+@pytest.mark.parametrize("name", [n for n in NAMES if n != "route"])
+def test_outputs_that_require_a_gradient_are_refused(host, name):
+    """A call that writes a tensor has no gradient for it: refused before anything is enqueued, as torch refuses
+    out= (with gradients off it is written)."""
+    call, written = next((c, w) for n, c, w in _calls() if n == name)
+    marked = [t for t in written if t.dtype == torch.float32]
+    for t in marked:
+        t.requires_grad_()
+        before = t._version
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call(*written)
+        assert t._version == before and t.requires_grad
+        with torch.no_grad():
+            call(*written)
+        call(*(w.detach() for w in written))
+        t.requires_grad_(False)
+    assert marked or name.startswith("fp4_quantize") or name == "fp4_swiglu"
