@@ -10,6 +10,7 @@ import ctypes
 import os
 
 import torch
+from torch.autograd import forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
@@ -153,10 +154,19 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+def _no_tangent(**tensors) -> None:
+    """The calls have no derivative in forward mode. (Its level first, -1 outside: asking a tensor costs 0.6 us.)"""
+    if forward_ad._current_level >= 0:
+        for name, t in tensors.items():
+            if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError(f"{name}: carries a tangent (no derivative in forward mode)")
+
+
 def _writable(name: str, t) -> None:
     """The calls have no gradient for what they write."""
     if isinstance(t, torch.Tensor) and t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name}: is written and requires a gradient (pass {name}.detach())")
+    _no_tangent(**{name: t})
 
 
 def _written(*given) -> None:
@@ -324,8 +334,9 @@ def workspace_view(d: MoeDims, T: int, ws: torch.Tensor, which: str, dtype, shap
 # (inputs written before, results read after, there or elsewhere) is the caller's.
 # Outputs that are given (out, codes, scales, grad_rows) count as written; one that
 # requires a gradient is refused.
-# Only balance_loss, gather_rows and combine_rows are recorded for autograd; the
-# 8-bit and 4-bit calls have no gradient, and what they return requires none.
+# Only balance_loss, gather_rows and combine_rows are recorded for autograd, for
+# its reverse mode (they refuse a tangent of forward mode); the 8-bit and 4-bit
+# calls have no gradient, and what they return requires none.
 TYPE_BF16, TYPE_F32 = 0, 1  # MOE_TYPE_*
 SUM_F32 = 0x100  # MOE_SUM_F32
 _FLOATS = {torch.bfloat16: TYPE_BF16, torch.int16: TYPE_BF16, torch.float32: TYPE_F32}  # int16: bf16 bits
@@ -721,6 +732,7 @@ def gather_rows(x: torch.Tensor, routes: dict, out=None, zero_rest: bool = False
     current here), and those behind the last route are zeros; out is not taken.
     Not while a graph is captured: there pass x.detach() and call
     gather_rows_backward."""
+    _no_tangent(x=x)
     if x.requires_grad and torch.is_grad_enabled():
         _no_capture(x, "x", "gather_rows_backward")
         _need(out is None, "out: not with an x that requires a gradient")
@@ -780,6 +792,7 @@ def combine_rows(rows: torch.Tensor, routes: dict, w=None, out_dtype=None, out=N
     stream that was current here); rows behind the last route get zeros. out is
     not taken then, and not while a graph is captured: there pass detached
     tensors and call combine_rows_backward."""
+    _no_tangent(rows=rows, w=w)
     if torch.is_grad_enabled():
         for name, t in (("rows", rows), ("w", w)):
             if t is not None and t.requires_grad:
@@ -874,6 +887,7 @@ def balance_loss(logits: torch.Tensor, ids: torch.Tensor, mask=None, ws=None, st
     own counts, once, on the stream that was current here; without the router
     weights' part, which is balance_loss_backward's). Not while a graph is
     captured: there pass logits.detach() and call balance_loss_backward."""
+    _no_tangent(logits=logits)
     if logits.requires_grad and torch.is_grad_enabled():
         # (autograd would take the gradient to leaves whose accumulation is bound to the stream of an eager pass)
         with torch.cuda.device(_device(logits)):

@@ -24,7 +24,8 @@ def host(monkeypatch):
     fine = lambda *a: B.MOE_OK
     names = ["route", "latent_forward", "latent_forward_timed", "latent_forward_routed", "latent_forward_persistent",
              "latent_forward_noalloc", "block_forward"]
-    monkeypatch.setattr(B, "_lib", types.SimpleNamespace(**{"moe_" + n: fine for n in names}))
+    monkeypatch.setattr(B, "_lib", types.SimpleNamespace(moe_balance_workspace_bytes=lambda *a: 0,
+                                                         **{"moe_" + n: fine for n in names}))
 
 
 def _routes(T=4, K=2, E=2):
@@ -114,3 +115,29 @@ def test_outputs_that_require_a_gradient_are_refused(host, name):
         call(*(w.detach() for w in written))
         t.requires_grad_(False)
     assert marked or name.startswith("fp4_quantize") or name == "fp4_swiglu"
+
+
+def _carrying():
+    """(name, call of a tensor that carries a tangent, its shape) for every differentiable argument of the calls that
+    are recorded for autograd"""
+    routes, x, rows, wt = _routes(), torch.zeros((4, 256)), torch.zeros((8, 256)), torch.zeros((4, 2))
+    ids = torch.zeros((70, 2), dtype=I32)
+    yield "gather_rows x", lambda t: B.gather_rows(t, routes), (4, 256)
+    yield "combine_rows rows", lambda t: B.combine_rows(t, routes, wt), (8, 256)
+    yield "combine_rows w", lambda t: B.combine_rows(rows, routes, t), (4, 2)
+    yield "balance_loss logits", lambda t: B.balance_loss(t, ids), (70, 8)
+    yield "gather_rows out", lambda t: B.gather_rows(x, routes, out=t), (8, 256)
+    yield "combine_rows out", lambda t: B.combine_rows(rows, routes, wt, out=t), (4, 256)
+
+
+@pytest.mark.parametrize("name", [c[0] for c in _carrying()])
+def test_tangents_are_refused(host, name):
+    """No call has a derivative in forward mode; none drops a tangent, or leaves one beside other values, in silence."""
+    call, shape = next((c, s) for n, c, s in _carrying() if n == name)
+    with torch.autograd.forward_ad.dual_level():
+        dual = torch.autograd.forward_ad.make_dual(torch.zeros(shape), torch.ones(shape))
+        for grad in (True, False):  # (forward mode goes on where gradients are off)
+            with torch.set_grad_enabled(grad), pytest.raises(ValueError, match="tangent"):
+                call(dual)
+        call(torch.zeros(shape))  # (inside a level, without a tangent)
+    call(torch.zeros(shape))
