@@ -790,14 +790,16 @@ def combine_rows(rows: torch.Tensor, routes: dict, w=None, out_dtype=None, out=N
 
     Where rows or w require a gradient, the result carries it (once, on the
     stream that was current here); rows behind the last route get zeros. out is
-    not taken then, and not while a graph is captured: there pass detached
-    tensors and call combine_rows_backward."""
+    not taken then, nor int16 (bf16 bits) for the result, and not while a graph
+    is captured: there pass detached tensors and call combine_rows_backward."""
     _no_tangent(rows=rows, w=w)
     if torch.is_grad_enabled():
         for name, t in (("rows", rows), ("w", w)):
             if t is not None and t.requires_grad:
                 _no_capture(rows, name, "combine_rows_backward")
                 _need(out is None, "out: not with tensors that require a gradient")
+                _need((rows.dtype if out_dtype is None else out_dtype) != torch.int16,
+                      f"out_dtype: {name} requires a gradient, which int16 (bf16 bits) cannot carry")
                 return _CombineRows.apply(rows, routes["offsets"], routes["positions"], w, out_dtype, stream)
     return _combine_rows(rows, routes, w, out_dtype, out, stream)
 

@@ -141,3 +141,20 @@ def test_tangents_are_refused(host, name):
                 call(dual)
         call(torch.zeros(shape))  # (inside a level, without a tangent)
     call(torch.zeros(shape))
+
+
+def test_a_result_that_cannot_carry_a_gradient_is_refused(host):
+    """Rows of bf16 bits held as int16: torch takes such a result for a constant, and the weights would get no gradient."""
+    routes, w = _routes(), torch.zeros((4, 2), requires_grad=True)
+    bits = torch.zeros((8, 256), dtype=torch.int16)
+    for rows, dtype in ((bits, None), (bits, torch.int16), (torch.zeros((8, 256)), torch.int16)):
+        with pytest.raises(ValueError, match="gradient"):
+            B.combine_rows(rows, routes, w, dtype)
+        with torch.no_grad():
+            assert B.combine_rows(rows, routes, w, dtype).dtype == torch.int16
+    for dtype in (torch.float32, torch.bfloat16):
+        y = B.combine_rows(bits, routes, w, dtype)
+        assert y.requires_grad
+        y.sum().backward()
+        assert w.grad.shape == w.shape
+    assert not B.combine_rows(bits, routes, w.detach()).requires_grad
