@@ -556,7 +556,9 @@ int moe_sort_routes(int32_t T, int32_t n_experts, int32_t top_k,
  * Positions outside [0, rows) are none; no two may be the same row (that row
  * is then unspecified). n_taken: NULL, and rows that no position names are left
  * as they were; or a device int32 (moe_sort_routes' expert_offsets[n_experts]),
- * and rows from *n_taken on become zeros.
+ * and rows from *n_taken on become zeros (no position may name one of them: that
+ * row is then unspecified). Rows before it that no position names are left as
+ * they were.
  * cols 1 .. 65536, top_k <= 8, T * top_k and rows below 2^28, pitches in
  * elements up to 2^22. Pointers need the alignment of their type only (rows of
  * a multiple of 8 values, all 16-byte aligned, are fastest). */

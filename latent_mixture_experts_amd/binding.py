@@ -454,8 +454,8 @@ def _quantize(what: str, x: torch.Tensor, cols: int, codes, scales, stream):
 
 
 def fp8_quantize(x: torch.Tensor, codes=None, scales=None, stream=None):
-    """moe_fp8_quantize of x [rows][cols] (bf16 or fp32, rows at any pitch):
-    (codes [rows][cols] e4m3, scales [rows][ceil(cols/128)] fp32)."""
+    """moe_fp8_quantize of x [rows][cols] (bf16 or fp32, every row at a multiple
+    of 16 bytes): (codes [rows][cols] e4m3, scales [rows][ceil(cols/128)] fp32)."""
     _need(x.dim() == 2, "x: needs two dimensions")
     return _quantize("moe_fp8_quantize", x, x.shape[1], codes, scales, stream)
 
@@ -481,8 +481,8 @@ def fp8_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
                out_dtype=torch.bfloat16, out=None, stream=None, f32_sums: bool = False) -> torch.Tensor:
     """moe_fp8_linear: x [T][K] e4m3 with x_scales [T][ceil(K/128)], times w
     [N][K] e4m3 with w_scales [ceil(N/128)][ceil(K/128)] -> [T][N] of
-    out_dtype, or into out. Rows of x and out at any pitch. f32_sums: a bf16
-    out, too, sums in fp32 throughout (MOE_SUM_F32)."""
+    out_dtype, or into out. Rows of x at multiples of 16 bytes, rows of out at
+    any pitch. f32_sums: a bf16 out, too, sums in fp32 throughout (MOE_SUM_F32)."""
     _need(x.dim() == 2 and w.dim() == 2, "x, w: need two dimensions")
     dev = _device(x)
     (T, K), N = x.shape, w.shape[0]
@@ -571,9 +571,9 @@ def _fp4_quantize(what: str, x: torch.Tensor, cols: int, codes, scales, stream):
 
 
 def fp4_quantize(x: torch.Tensor, codes=None, scales=None, stream=None):
-    """moe_fp4_quantize of x [rows][cols] (bf16 or fp32, rows at any pitch):
-    (codes [rows][cols/2] uint8, two E2M1 values a byte; scales [rows][cols/32]
-    uint8, E8M0): the layer's MXFP4, also for its weights."""
+    """moe_fp4_quantize of x [rows][cols] (bf16 or fp32, every row at a multiple
+    of 16 bytes): (codes [rows][cols/2] uint8, two E2M1 values a byte; scales
+    [rows][cols/32] uint8, E8M0): the layer's MXFP4, also for its weights."""
     _need(x.dim() == 2, "x: needs two dimensions")
     return _fp4_quantize("moe_fp4_quantize", x, x.shape[1], codes, scales, stream)
 
@@ -609,7 +609,7 @@ def fp4_linear(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scale
                out_dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
     """moe_fp4_linear: x [T][K/2] with x_scales [T][K/32] times w [N][K/2] with
     w_scales [N][K/32], as fp4_quantize gives them -> [T][N] of out_dtype, or
-    into out. Rows of x and out at any pitch."""
+    into out. Rows of x at multiples of 16 bytes, rows of out at any pitch."""
     _need(x.dim() == 2 and w.dim() == 2, "x, w: need two dimensions")
     dev = _device(x)
     (T, half), N = x.shape, w.shape[0]
@@ -724,9 +724,9 @@ def _once(what: str) -> None:
 
 def gather_rows(x: torch.Tensor, routes: dict, out=None, zero_rest: bool = False, stream=None) -> torch.Tensor:
     """moe_gather_rows: x [T][cols] (bf16 or fp32, rows at any pitch) into the
-    order of routes (sort_routes' dict; offsets and positions are read): [T*K]
-    rows, or into out [rows][cols]. Rows behind the last route are left as they
-    are (as allocated, without out), or zeros with zero_rest.
+    order of routes (sort_routes' dict as it came; offsets and positions are
+    read): [T*K] rows, or into out [rows][cols]. Rows behind the last route are
+    left as they are (as allocated, without out), or zeros with zero_rest.
 
     Where x requires a gradient, the rows carry it (once, on the stream that was
     current here), and those behind the last route are zeros; out is not taken.
