@@ -166,15 +166,19 @@ def _writable(name: str, t) -> None:
     """The calls have no gradient for what they write."""
     if isinstance(t, torch.Tensor) and t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name}: is written and requires a gradient (pass {name}.detach())")
-    _no_tangent(**{name: t})
+    if forward_ad._current_level >= 0:
+        _no_tangent(**{name: t})
+
+
+_increment_version = torch.autograd.graph.increment_version
 
 
 def _written(*given) -> None:
     """Counts a write of the caller's tensors (None: not given), as torch's own calls
     do: a backward pass that saved them before this call refuses to run on what they hold now."""
-    given = [t for t in given if isinstance(t, torch.Tensor)]
-    if given:
-        torch.autograd.graph.increment_version(given)
+    for t in given:
+        if isinstance(t, torch.Tensor):
+            _increment_version(t)
 
 
 def _stream(stream) -> int:
