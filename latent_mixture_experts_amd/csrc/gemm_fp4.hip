@@ -11,10 +11,12 @@
 // them, a scale of 255 gives NaN).
 //
 // What bounds it: one to 16 rows, the weights' way from HBM and a launch's start
-// (4096 x 8192: 6.4 us); few rows per expert, HBM (32 tokens' down projection, 163
-// experts of 4096 x 4096, 1.45 GB: 219 us, 6.6 TB/s); thousands of rows, the
-// operands' way from L2 into LDS (4096 x 4096 x 8192: 67 us, 4.1 PFLOP/s, of which
-// the matrix unit is busy 27 us at 2.4 GHz; 806 MB pass into LDS at 12 TB/s).
+// (4096 x 8192: 6.7 us); few rows per expert, HBM (32 tokens' down projection, 163
+// experts of 4096 x 4096, 1.45 GB: 219 us, 6.6 TB/s); thousands of rows, the latency
+// of the copies from L2 into LDS with two stages held (4096 x 4096 x 8192: 67 us,
+// 4.1 PFLOP/s, of which the matrix unit is busy 27 us at 2.4 GHz and LDS three
+// tenths of the time; 570 MB pass into LDS at 8.5 TB/s, in 6.3e6 requests to L2, a
+// third of them for 16 bytes of scales each).
 #include <algorithm>
 #include <cmath>
 
@@ -625,6 +627,9 @@ hipError_t launch_tile_as(const Fp4Gemm& g, hipStream_t st) {
   // many tiles read do not (4096 dense rows 93 -> 99). Experts get their rows unevenly:
   // where more than about four in ten start a second row tile the weights of those
   // cost more than that gains (128 rows on average in tiles of 128: 622 -> 715 us).
+  // Only the mean is known here, and skewed routing takes what it asks for: with half
+  // of the routes on 16 of 256 experts of 4096 x 4096, 512 tokens take 433 us (routed
+  // evenly 430), 4096 tokens 677 (591); 512 tokens on 8192 x 4096 943 (891).
   const dim3 block(64 * WT * WW * KG);
   const double mean = static_cast<double>(g.rows) / g.experts;
   if (SCALES != kBy1 && (g.experts > 1 ? mean + 0.3 * std::sqrt(mean) : mean) <= BM)
@@ -655,9 +660,10 @@ hipError_t launch_tile(const Fp4Gemm& g, hipStream_t st) {
 //   2048    207    114    107      67       53          45             41       57
 //   4096    386    209    186     124      106          88             82       67
 // Small tiles win while they fit one round, their stages being mostly latency;
-// for thousands of rows what counts is how often an operand enters LDS (about
-// 14 TB/s over the chip at best). N = 8192, K = 4096, 4096 rows: 128x256 96, 256x256
-// 76. Experts of 128 rows (4096 tokens' down projection): 654, 622 and 576 with the last
+// for thousands of rows what counts is how often an operand enters LDS (12 .. 16
+// TB/s over the chip with tiles of up to 128 x 128, 10 with 128 x 256, 8.5 with 256 x
+// 256, whose stages wait for their copies' latency). N = 8192, K = 4096, 4096 rows:
+// 128x256 96, 256x256 76. Experts of 128 rows (4096 tokens' down projection): 654, 622 and 576 with the last
 // three. Over 13 widths, dense and per expert, 1 .. 4096 rows, the choice costs at
 // most 1.15 times the best of them.
 struct TileCost {
@@ -714,6 +720,9 @@ int best_tile(const Fp4Gemm& g) {
 //      1   5.2 / 7.5    6.8 / 8.9   6.1 / 7.1    4.5 / 5.3    31.6 / 30.6   7.4 / 8.7
 //      8        -       7.5 / 9.1       -        4.8 / 5.4    37.9 / 31.3       -
 //     16   6.6 / 8.6    8.4 / 9.4   8.0 / 7.2    5.2 / 5.6    45.2 / 31.6  10.0 / 8.9
+// The step at N = 4096 is where a second workgroup joins a CU. Over N = 4096 .. 12288,
+// K = 1024, 4096 and 8192, 1 .. 16 rows, the limits cost at most 1.11 times the better
+// kernel (4112 x 4096, 8 rows: 5.9 / 6.5, and tiles taken).
 // Per expert the tiles are level with it (8 routes of one token, N = 4096, K =
 // 4096: 18.9 / 16.4) or better (32 tokens' 163 experts 296 / 252).
 bool streams(const Fp4Gemm& g) {

@@ -15,9 +15,11 @@
 // and conversion. A lane holds 8 values (16-byte loads of bf16, 4-byte stores),
 // a group is four lanes, its maximum two DPP steps, the conversion instruction
 // takes the scale. Loads of values, and stores of them on the way back, pass the
-// caches by (4096 x 8192 there and back 31.4 -> 30.4 us, SwiGLU 2% less). 4096 x 8192
-// bf16: 16 us, 5.3 TB/s, and back 12 us (codes from the cache); SwiGLU to 32768 x
-// 4096 bf16 101 us, 6.0 TB/s; 32 x 4096: 2.2 us, a launch.
+// caches by (4096 x 8192 there and back 31.4 -> 30.4 us, SwiGLU 2% less; back and
+// quantised again, 1024 rows 9.6 us, 9.5 with stores through the caches, 4096 rows 31.2
+// and 30.7, 16384 rows 110 and 114). 4096 x 8192 bf16: 16 .. 18 us, 5 TB/s, and back
+// 12 us (codes from the cache); SwiGLU to 32768 x 4096 bf16 101 us, 6.0 TB/s; 32 x
+// 4096: 2.2 us, a launch.
 #include "device_common.h"
 #include "fp4.h"
 #include "kernels.h"
